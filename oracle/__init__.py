@@ -14,6 +14,7 @@ It restates, plainly and slowly, what the source pages define:
   quantizer uniform asymmetric / symmetric quantizer, group and per-row statistics, RTN
   pack      LSB-first bit packing of the codes, fp16 scales/zeros
   error     the layer objective ||W X - W_hat X||_F^2
+  fp8       the e4m3 format with block scales, and the norm and products on it
 
 Page titles cited in the docstrings (section names follow each title):
   [INT4-GPTQ]  "INT4 and GPTQ Quantization" (beta.fermi.ai wiki)
@@ -29,5 +30,5 @@ in float32 with IEEE division and round-half-to-even.
 Parity status of each function is stated in its docstring ("pinned by ..."). Functions with
 no external pin say "parity unpinned".
 """
-from . import error, gemv, hessian, pack, prepare, quantizer, sweep  # noqa: F401
+from . import error, fp8, gemv, hessian, pack, prepare, quantizer, sweep  # noqa: F401
 from .layer import gptq_layer, rtn_layer  # noqa: F401

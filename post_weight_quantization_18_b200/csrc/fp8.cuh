@@ -1,0 +1,181 @@
+// fp8.cuh — what the 8-bit floating point kernels share: the e4m3 conversions, the scale of a
+// block, and loads and stores of 16- and 32-bit elements as fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/fp8.h"
+#include "common.cuh"
+
+namespace gptq {
+
+constexpr int kFp8Block = 128;           // columns (and weight rows) that share one scale
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: 1 / s stays finite
+
+// Two fp32 values -> two e4m3 bytes (a in the low byte), round to nearest even, +-448 beyond.
+GPTQ_DEV uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+GPTQ_DEV uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+// Two e4m3 bytes (low 16 bits of v) -> fp16 pair; exact.
+GPTQ_DEV __half2 e4m3x2_to_half2(uint32_t v) {
+  uint32_t r;
+  const uint16_t h = (uint16_t)v;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
+  return *reinterpret_cast<__half2*>(&r);
+}
+
+// Magnitude as an unsigned number whose order is that of |v|, infinities and NaNs on top: the
+// maximum of these finds both the block's largest value and whether anything is not finite.
+GPTQ_DEV uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The scale of a block from the largest mag_bits of its values, and the factor 1 / s.
+GPTQ_DEV void block_scale(uint32_t amax_bits, float& s, float& inv) {
+  if (amax_bits >= 0x7F800000u) {
+    s = inv = __uint_as_float(0x7FC00000u);
+  } else if (amax_bits == 0u) {
+    s = inv = 1.f;
+  } else {
+    s = fmaxf(__fdiv_rn(__uint_as_float(amax_bits), kE4m3Max), kMinScale);
+    inv = __frcp_rn(s);
+  }
+}
+
+template <typename T>
+GPTQ_DEV float to_f32(T v);
+template <>
+GPTQ_DEV float to_f32<float>(float v) { return v; }
+template <>
+GPTQ_DEV float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+GPTQ_DEV float to_f32<__half>(__half v) { return __half2float(v); }
+
+template <typename T>
+GPTQ_DEV T from_f32(float v);
+template <>
+GPTQ_DEV float from_f32<float>(float v) { return v; }
+template <>
+GPTQ_DEV __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+GPTQ_DEV __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// Eight consecutive elements, as loaded.
+template <typename T>
+struct Vec8 {
+  static constexpr int kWords = (int)sizeof(T) * 2;  // 32-bit words
+  uint32_t w[kWords];
+  GPTQ_DEV float get(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[i]);
+    } else {
+      const uint16_t h = (uint16_t)(w[i >> 1] >> ((i & 1) * 16));
+      return to_f32<T>(*reinterpret_cast<const T*>(&h));
+    }
+  }
+  GPTQ_DEV void set(int i, float v) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(v);
+    } else {
+      const T t = from_f32<T>(v);
+      const uint32_t h = *reinterpret_cast<const uint16_t*>(&t);
+      w[i >> 1] = (i & 1) ? (w[i >> 1] | (h << 16)) : h;
+    }
+  }
+};
+
+// `valid` (0..8) elements at p, zeros behind them. vec: p is 16-byte aligned.
+template <typename T>
+GPTQ_DEV Vec8<T> load8(const T* p, int valid, bool vec) {
+  Vec8<T> v;
+#pragma unroll
+  for (int i = 0; i < Vec8<T>::kWords; ++i) v.w[i] = 0u;
+  if (vec && valid == 8) {
+#pragma unroll
+    for (int i = 0; i < Vec8<T>::kWords; i += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+      v.w[i] = q.x; v.w[i + 1] = q.y; v.w[i + 2] = q.z; v.w[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) v.set(i, to_f32<T>(p[i]));
+  }
+  return v;
+}
+template <typename T>
+GPTQ_DEV void store8(T* p, const Vec8<T>& v, int valid, bool vec) {
+  if (vec && valid == 8) {
+#pragma unroll
+    for (int i = 0; i < Vec8<T>::kWords; i += 4)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) =
+          make_uint4(v.w[i], v.w[i + 1], v.w[i + 2], v.w[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = from_f32<T>(v.get(i));
+  }
+}
+// Eight e4m3 bytes; vec: p is 8-byte aligned.
+GPTQ_DEV void store_q8(uint8_t* p, uint2 q, int valid, bool vec) {
+  if (vec && valid == 8) {
+    *reinterpret_cast<uint2*>(p) = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) p[i] = (uint8_t)((i < 4 ? q.x : q.y) >> ((i & 3) * 8));
+  }
+}
+
+// One output value of the products.
+GPTQ_DEV void store_out(void* Y, long long at, float v, int dtype) {
+  if (dtype == GPTQ_F32)
+    reinterpret_cast<float*>(Y)[at] = v;
+  else if (dtype == GPTQ_BF16)
+    reinterpret_cast<__nv_bfloat16*>(Y)[at] = __float2bfloat16_rn(v);
+  else
+    reinterpret_cast<__half*>(Y)[at] = __float2half_rn(v);
+}
+
+// The gated activation in fp32: g * sigmoid(g) * u. exp(-g) overflows to infinity below
+// g = -88.7, where the quotient is then the correct -0.
+GPTQ_DEV float silu_mul(float g, float u) { return __fdiv_rn(g, 1.f + expf(-g)) * u; }
+
+}  // namespace gptq
+
+namespace gptq_host {
+
+struct Fp8Gemm {  // arguments of one product, or of the gated pair (w1 != nullptr)
+  const uint8_t* x;
+  long long ldx;
+  const float* sx;
+  long long ldsx;
+  const uint8_t* w[2];
+  long long ldw[2];
+  const float* sw[2];
+  long long ldsw[2];
+  int m, n, k;
+  void* y;        // Y, or Q of the gated pair
+  int y_dtype;    // of Y
+  long long ldy;
+  float* sy;      // the gated pair's scales
+  long long ldsy;
+  int32_t* status;
+};
+
+int fp8_quantize_rows(const void* x, int dtype, long long ldx, int m, int k, uint8_t* q,
+                      long long ldq, float* s, long long lds, cudaStream_t stream);
+int fp8_quantize_blocks(const void* x, int dtype, long long ldx, int m, int k, uint8_t* q,
+                        long long ldq, float* s, long long lds, cudaStream_t stream);
+int fp8_add_rmsnorm(const void* x, long long ldx, const void* r, long long ldr, int dtype,
+                    const void* gamma, int gamma_dtype, float eps, int m, int k, void* h,
+                    long long ldh, uint8_t* q, long long ldq, float* s, long long lds,
+                    cudaStream_t stream);
+int fp8_gemm_simt(const Fp8Gemm& a, cudaStream_t stream);
+
+}  // namespace gptq_host
