@@ -177,5 +177,8 @@ int fp8_add_rmsnorm(const void* x, long long ldx, const void* r, long long ldr, 
                     long long ldh, uint8_t* q, long long ldq, float* s, long long lds,
                     cudaStream_t stream);
 int fp8_gemm_simt(const Fp8Gemm& a, cudaStream_t stream);
+// The tensor-core kernels, and whether TMA can address the operands.
+bool fp8_gemm_tc_takes(const Fp8Gemm& a);
+int fp8_gemm_tc(const Fp8Gemm& a, cudaStream_t stream);
 
 }  // namespace gptq_host

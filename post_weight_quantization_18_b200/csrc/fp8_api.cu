@@ -21,7 +21,9 @@ inline bool operand_ok(const uint8_t* q, const float* s) {
 }
 
 int gemm_launch(const gptq_host::Fp8Gemm& a, cudaStream_t stream) {
-  return gptq_host::fp8_gemm_simt(a, stream) ? GPTQ_ERR_CUDA : GPTQ_OK;
+  const int rc = gptq_host::fp8_gemm_tc_takes(a) ? gptq_host::fp8_gemm_tc(a, stream)
+                                                 : gptq_host::fp8_gemm_simt(a, stream);
+  return rc ? GPTQ_ERR_CUDA : GPTQ_OK;
 }
 
 }  // namespace
