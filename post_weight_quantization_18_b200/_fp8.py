@@ -24,36 +24,44 @@ _lib.fp8_gemm.argtypes = [_P, _I64, _P, _I64] * 2 + [_I64] * 3 + [_P, _I32, _I64
 _lib.fp8_gated_gemm.argtypes = [_P, _I64, _P, _I64] * 3 + [_I64] * 3 + [_P, _I64, _P, _I64, _P, _P]
 for _name in EXPORTED_FP8:
     getattr(_lib, _name).restype = _I32
+_quantize, _add_rmsnorm = _lib.fp8_quantize, _lib.fp8_add_rmsnorm
+_gemm, _gated_gemm = _lib.fp8_gemm, _lib.fp8_gated_gemm
+_raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 _DTYPES = {torch.bfloat16: GPTQ_BF16, torch.float32: GPTQ_F32, torch.float16: GPTQ_F16}
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, pitch: int = 1) -> int:
-    """The leading dimension of t, a [rows, cols] CUDA tensor with unit stride along its rows. One
-    row alone has no pitch: it counts as the next multiple of `pitch`."""
-    if not t.is_cuda:
+def _device(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    return dev
+
+
+def _matrix(t: torch.Tensor, name: str, dev: int, rows: int, cols: int, pitch: int = 1) -> int:
+    """The leading dimension of t, a [rows, cols] tensor of device `dev` with unit stride along its
+    rows. One row alone has no pitch: it counts as the next multiple of `pitch`."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, is on {t.device}")
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its last dim")
-    if rows <= 1:
-        return -(-cols // pitch) * pitch
-    return ld
+    return ld if rows > 1 else -(-cols // pitch) * pitch
 
 
-def _e4m3(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+def _e4m3(t: torch.Tensor, name: str, dev: int, rows: int, cols: int) -> int:
     if t.dtype not in _E4M3:
         raise ValueError(f"{name} must be float8_e4m3fn or uint8, got {t.dtype}")
-    return _matrix(t, name, rows, cols, 16)
+    return _matrix(t, name, dev, rows, cols, 16)
 
 
-def _scales(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+def _scales(t: torch.Tensor, name: str, dev: int, rows: int, cols: int) -> int:
     if t.dtype is not torch.float32:
         raise ValueError(f"{name} must be torch.float32, got {t.dtype}")
-    return _matrix(t, name, rows, cols)
+    return _matrix(t, name, dev, rows, cols)
 
 
 def _float_code(t: torch.Tensor, name: str) -> int:
@@ -66,31 +74,30 @@ def _float_code(t: torch.Tensor, name: str) -> int:
 def _shape2(t: torch.Tensor, name: str) -> tuple[int, int]:
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a tensor of 2 dims")
-    return t.shape[0], t.shape[1]
+    return t.shape
 
 
-def _status_ptr(t: torch.Tensor | None, dev: torch.device):
+def _status_ptr(t: torch.Tensor | None, dev: int):
     if t is None:
         return None
-    if not t.is_cuda or t.device != dev or t.dtype is not torch.int32 or t.numel() < 2 \
+    if t.get_device() != dev or t.dtype is not torch.int32 or t.numel() < 2 \
             or not t.is_contiguous():
         raise ValueError("dev_status must be a contiguous int32 CUDA tensor of 2 entries on the "
                          "operands' device")
     return t.data_ptr()
 
 
-def _call(fn, where: str, dev: torch.device, others, *args) -> None:
-    """fn(*args, stream) with the tensors' device current (they must share one)."""
-    for t in others:
-        if t.device != dev:
-            raise ValueError(f"{where}: tensors are on different devices ({dev} and {t.device})")
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+def _call(fn, dev: int, *args) -> None:
+    """fn(*args, stream): on the current stream of device `dev`, made current for the call. The raw
+    stream is asked for directly: torch.cuda.current_stream() builds a Stream object each time, 4.6
+    us on the host, as much as the launch itself."""
+    if dev == _get_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+            rc = fn(*args, _raw_stream(dev))
     if rc:
-        _check(rc, where)
+        _check(rc, fn.__name__)
 
 
 def fp8_quantize(X: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1
@@ -101,11 +108,12 @@ def fp8_quantize(X: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor, block_r
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
     code = _float_code(X, "X")
-    ldx = _matrix(X, "X", m, k, 8)
-    ldq = _e4m3(Q, "Q", m, k)
-    lds = _scales(scales, "scales", -(-m // block_rows), -(-k // 128))
-    _call(_lib.fp8_quantize, "fp8_quantize", X.device, (Q, scales), X.data_ptr(), code, ldx, m, k,
-          block_rows, Q.data_ptr(), ldq, scales.data_ptr(), lds)
+    dev = _device(X, "X")
+    ldx = _matrix(X, "X", dev, m, k, 8)
+    ldq = _e4m3(Q, "Q", dev, m, k)
+    lds = _scales(scales, "scales", dev, -(-m // block_rows), -(-k // 128))
+    _call(_quantize, dev, X.data_ptr(), code, ldx, m, k, block_rows, Q.data_ptr(), ldq,
+          scales.data_ptr(), lds)
 
 
 def fp8_add_rmsnorm(X: torch.Tensor, R: torch.Tensor | None, gamma: torch.Tensor, eps: float,
@@ -115,29 +123,26 @@ def fp8_add_rmsnorm(X: torch.Tensor, R: torch.Tensor | None, gamma: torch.Tensor
     m, k = _shape2(X, "X")
     code = _float_code(X, "X")
     gcode = _float_code(gamma, "gamma")
-    ldx = _matrix(X, "X", m, k, 8)
-    if not gamma.is_cuda or gamma.dim() != 1 or gamma.shape[0] != k or not gamma.is_contiguous():
-        raise ValueError("gamma must be a contiguous CUDA tensor of k entries")
-    others = [gamma, Q, scales]
+    dev = _device(X, "X")
+    ldx = _matrix(X, "X", dev, m, k, 8)
+    if gamma.get_device() != dev or gamma.shape != (k,) or not gamma.is_contiguous():
+        raise ValueError(f"gamma must be a contiguous CUDA tensor of {k} entries on device {dev}")
     r_ptr = h_ptr = None
     ldr = ldh = 0
     if R is not None:
         if R.dtype is not X.dtype:
             raise ValueError("R must have X's dtype")
-        ldr = _matrix(R, "R", m, k, 8)
+        ldr = _matrix(R, "R", dev, m, k, 8)
         r_ptr = R.data_ptr()
-        others.append(R)
     if H is not None:
         if H.dtype is not X.dtype:
             raise ValueError("H must have X's dtype")
-        ldh = _matrix(H, "H", m, k, 8)
+        ldh = _matrix(H, "H", dev, m, k, 8)
         h_ptr = H.data_ptr()
-        others.append(H)
-    ldq = _e4m3(Q, "Q", m, k)
-    lds = _scales(scales, "scales", m, -(-k // 128))
-    _call(_lib.fp8_add_rmsnorm, "fp8_add_rmsnorm", X.device, others, X.data_ptr(), ldx, r_ptr, ldr,
-          code, gamma.data_ptr(), gcode, float(eps), m, k, h_ptr, ldh, Q.data_ptr(), ldq,
-          scales.data_ptr(), lds)
+    ldq = _e4m3(Q, "Q", dev, m, k)
+    lds = _scales(scales, "scales", dev, m, -(-k // 128))
+    _call(_add_rmsnorm, dev, X.data_ptr(), ldx, r_ptr, ldr, code, gamma.data_ptr(), gcode, eps, m,
+          k, h_ptr, ldh, Q.data_ptr(), ldq, scales.data_ptr(), lds)
 
 
 def fp8_gemm(X: torch.Tensor, sx: torch.Tensor, W: torch.Tensor, sw: torch.Tensor,
@@ -147,13 +152,13 @@ def fp8_gemm(X: torch.Tensor, sx: torch.Tensor, W: torch.Tensor, sw: torch.Tenso
     m, k = _shape2(X, "X")
     n = _shape2(W, "W")[0]
     g = -(-k // 128)
-    ldx, ldsx = _e4m3(X, "X", m, k), _scales(sx, "sx", m, g)
-    ldw, ldsw = _e4m3(W, "W", n, k), _scales(sw, "sw", -(-n // 128), g)
+    dev = _device(X, "X")
+    ldx, ldsx = _e4m3(X, "X", dev, m, k), _scales(sx, "sx", dev, m, g)
+    ldw, ldsw = _e4m3(W, "W", dev, n, k), _scales(sw, "sw", dev, -(-n // 128), g)
     code = _float_code(Y, "Y")
-    ldy = _matrix(Y, "Y", m, n, 8)
-    _call(_lib.fp8_gemm, "fp8_gemm", X.device, (sx, W, sw, Y), X.data_ptr(), ldx, sx.data_ptr(),
-          ldsx, W.data_ptr(), ldw, sw.data_ptr(), ldsw, m, n, k, Y.data_ptr(), code, ldy,
-          _status_ptr(dev_status, X.device))
+    ldy = _matrix(Y, "Y", dev, m, n, 8)
+    _call(_gemm, dev, X.data_ptr(), ldx, sx.data_ptr(), ldsx, W.data_ptr(), ldw, sw.data_ptr(),
+          ldsw, m, n, k, Y.data_ptr(), code, ldy, _status_ptr(dev_status, dev))
 
 
 def fp8_gated_gemm(X: torch.Tensor, sx: torch.Tensor, Wg: torch.Tensor, sg: torch.Tensor,
@@ -164,11 +169,11 @@ def fp8_gated_gemm(X: torch.Tensor, sx: torch.Tensor, Wg: torch.Tensor, sg: torc
     m, k = _shape2(X, "X")
     n = _shape2(Wg, "Wg")[0]
     g, gn = -(-k // 128), -(-n // 128)
-    ldx, ldsx = _e4m3(X, "X", m, k), _scales(sx, "sx", m, g)
-    ldg, ldsg = _e4m3(Wg, "Wg", n, k), _scales(sg, "sg", gn, g)
-    ldu, ldsu = _e4m3(Wu, "Wu", n, k), _scales(su, "su", gn, g)
-    ldq, lds = _e4m3(Q, "Q", m, n), _scales(scales, "scales", m, gn)
-    _call(_lib.fp8_gated_gemm, "fp8_gated_gemm", X.device, (sx, Wg, sg, Wu, su, Q, scales),
-          X.data_ptr(), ldx, sx.data_ptr(), ldsx, Wg.data_ptr(), ldg, sg.data_ptr(), ldsg,
-          Wu.data_ptr(), ldu, su.data_ptr(), ldsu, m, n, k, Q.data_ptr(), ldq, scales.data_ptr(),
-          lds, _status_ptr(dev_status, X.device))
+    dev = _device(X, "X")
+    ldx, ldsx = _e4m3(X, "X", dev, m, k), _scales(sx, "sx", dev, m, g)
+    ldg, ldsg = _e4m3(Wg, "Wg", dev, n, k), _scales(sg, "sg", dev, gn, g)
+    ldu, ldsu = _e4m3(Wu, "Wu", dev, n, k), _scales(su, "su", dev, gn, g)
+    ldq, lds = _e4m3(Q, "Q", dev, m, n), _scales(scales, "scales", dev, m, gn)
+    _call(_gated_gemm, dev, X.data_ptr(), ldx, sx.data_ptr(), ldsx, Wg.data_ptr(), ldg,
+          sg.data_ptr(), ldsg, Wu.data_ptr(), ldu, su.data_ptr(), ldsu, m, n, k, Q.data_ptr(), ldq,
+          scales.data_ptr(), lds, _status_ptr(dev_status, dev))

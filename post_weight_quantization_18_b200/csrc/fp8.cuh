@@ -177,8 +177,16 @@ int fp8_add_rmsnorm(const void* x, long long ldx, const void* r, long long ldr, 
                     long long ldh, uint8_t* q, long long ldq, float* s, long long lds,
                     cudaStream_t stream);
 int fp8_gemm_simt(const Fp8Gemm& a, cudaStream_t stream);
-// The tensor-core kernels, and whether TMA can address the operands.
-bool fp8_gemm_tc_takes(const Fp8Gemm& a);
-int fp8_gemm_tc(const Fp8Gemm& a, cudaStream_t stream);
+// Whether TMA can address the operands, as the kernels below want them.
+bool fp8_tma_takes(const Fp8Gemm& a);
+// The tensor-core kernels: bound by the arithmetic, and for few rows of activations, bound by the
+// weight's bytes; with the time each needs for a block of 128 columns of K, in units of 1.7 ns.
+int fp8_gemm_wide(const Fp8Gemm& a, cudaStream_t stream);
+long long fp8_wide_cost(const Fp8Gemm& a);
+int fp8_thin(const Fp8Gemm& a, cudaStream_t stream);
+long long fp8_thin_cost(const Fp8Gemm& a);
+// A tensor map of whole blocks of 128 columns: boxes of 128 bytes x box_rows x box_blocks.
+int make_tmap_blocks(CUtensorMap* map, const uint8_t* base, uint64_t rows, uint64_t ld,
+                     uint64_t blocks, uint32_t box_rows, uint32_t box_blocks);
 
 }  // namespace gptq_host

@@ -21,8 +21,10 @@ inline bool operand_ok(const uint8_t* q, const float* s) {
 }
 
 int gemm_launch(const gptq_host::Fp8Gemm& a, cudaStream_t stream) {
-  const int rc = gptq_host::fp8_gemm_tc_takes(a) ? gptq_host::fp8_gemm_tc(a, stream)
-                                                 : gptq_host::fp8_gemm_simt(a, stream);
+  const int rc = !gptq_host::fp8_tma_takes(a) ? gptq_host::fp8_gemm_simt(a, stream)
+                 : gptq_host::fp8_wide_cost(a) < gptq_host::fp8_thin_cost(a)
+                     ? gptq_host::fp8_gemm_wide(a, stream)
+                     : gptq_host::fp8_thin(a, stream);
   return rc ? GPTQ_ERR_CUDA : GPTQ_OK;
 }
 

@@ -248,3 +248,28 @@ def test_linear_on_quantized_layer_has_the_formats_error():
     assert np.all(np.abs(f64(Y) - ref) <= gemm_bound(A, k) + np.abs(ref) * 2.0 ** -24)
     np.testing.assert_allclose(f64(x.dequantize()) @ f64(w.dequantize()).T, ref, rtol=0,
                                atol=float(A.max()) * 2.0 ** -22)
+
+
+def test_binding_refuses_wrong_operands():
+    import post_weight_quantization_18_b200 as G
+    q = torch.zeros((4, 256), dtype=torch.uint8, device="cuda")
+    s, sw = torch.zeros((4, 2), device="cuda"), torch.zeros((1, 2), device="cuda")
+    Y = torch.zeros((4, 4), device="cuda")
+    with pytest.raises(ValueError, match="float8_e4m3fn or uint8"):
+        G.fp8_gemm(q.to(torch.int32), s, q, sw, Y)
+    with pytest.raises(ValueError, match=r"sw must be \[1, 2\]"):
+        G.fp8_gemm(q, s, q, s, Y)
+    with pytest.raises(ValueError, match="torch.float32"):
+        G.fp8_gemm(q, s.half(), q, sw, Y)
+    with pytest.raises(ValueError, match=r"W must be \[4, 256\]"):
+        G.fp8_gemm(q, s, q[:, :128], sw, Y)
+    with pytest.raises(ValueError, match=r"Y must be \[4, 4\]"):
+        G.fp8_gemm(q, s, q, sw, Y[:3])
+    with pytest.raises(ValueError, match="CUDA"):
+        G.fp8_gemm(q, s, q.cpu(), sw, Y)
+    with pytest.raises(ValueError, match="dev_status"):
+        G.fp8_gemm(q, s, q, sw, Y, torch.zeros(2, device="cuda"))
+    with pytest.raises(ValueError, match="unit stride"):
+        G.fp8_gemm(q, s, q, sw, torch.zeros((4, 4), device="cuda").t())
+    with pytest.raises(ValueError, match=r"Q must be \[4, 4\]"):
+        G.fp8_gated_gemm(q, s, q, sw, q, sw, q, s)
