@@ -14,6 +14,15 @@ constexpr int kFp8Block = 128;           // columns (and weight rows) that share
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: 1 / s stays finite
 
+// The kernels here are launched so that one may start while the kernel before it in the stream still
+// runs (fp8_launch): they set up what is their own, then wait for that kernel and its writes. Every
+// thread calls this before it reads or writes memory that a caller owns.
+GPTQ_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel in the stream start (it waits as above).
+GPTQ_DEV void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Two fp32 values -> two e4m3 bytes (a in the low byte), round to nearest even, +-448 beyond.
 GPTQ_DEV uint32_t e4m3x2(float a, float b) {
   uint16_t r;
@@ -142,13 +151,40 @@ GPTQ_DEV void store_out(void* Y, long long at, float v, int dtype) {
     reinterpret_cast<__half*>(Y)[at] = __float2half_rn(v);
 }
 
-// The gated activation in fp32: g * sigmoid(g) * u. exp(-g) overflows to infinity below
-// g = -88.7, where the quotient is then the correct -0.
-GPTQ_DEV float silu_mul(float g, float u) { return __fdiv_rn(g, 1.f + expf(-g)) * u; }
+// The gated activation in fp32: g * sigmoid(g) * u. exp(-g) overflows to infinity below g = -88.7,
+// where the quotient is then the correct -0. The approximate quotient (2 ulp) keeps h within
+// 8 * 2^-24 of itself: expf 2, the sum 1, the quotient 4, the product 1.
+GPTQ_DEV float silu_mul(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
 
 }  // namespace gptq
 
 namespace gptq_host {
+
+// Launch in clusters of `cluster` CTAs (1: none), with `smem` bytes of dynamic shared memory, allowed
+// to start before the previous kernel of the stream has ended. Back to back the kernels of a decoding
+// step are 2 to 3 us apart otherwise: the launch, and the set-up of barriers and tensor memory.
+template <typename... P, typename... A>
+int fp8_launch(void (*kernel)(P...), long long grid, int threads, int smem, int cluster,
+               cudaStream_t stream, const A&... args) {
+  if (grid < 1 || grid > 0x7FFFFFFFll) return GPTQ_ERR_CUDA;
+  if (smem > 48 * 1024 && ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem) != 0)
+    return GPTQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? 0
+                                                                                  : GPTQ_ERR_CUDA;
+}
 
 struct Fp8Gemm {  // arguments of one product, or of the gated pair (w1 != nullptr)
   const uint8_t* x;
@@ -185,6 +221,7 @@ int fp8_gemm_wide(const Fp8Gemm& a, cudaStream_t stream);
 long long fp8_wide_cost(const Fp8Gemm& a);
 int fp8_thin(const Fp8Gemm& a, cudaStream_t stream);
 long long fp8_thin_cost(const Fp8Gemm& a);
+int fp8_skinny(const Fp8Gemm& a, cudaStream_t stream);  // up to 32 rows
 // A tensor map of whole blocks of 128 columns: boxes of 128 bytes x box_rows x box_blocks.
 int make_tmap_blocks(CUtensorMap* map, const uint8_t* base, uint64_t rows, uint64_t ld,
                      uint64_t blocks, uint32_t box_rows, uint32_t box_blocks);

@@ -22,6 +22,7 @@ inline bool operand_ok(const uint8_t* q, const float* s) {
 
 int gemm_launch(const gptq_host::Fp8Gemm& a, cudaStream_t stream) {
   const int rc = !gptq_host::fp8_tma_takes(a) ? gptq_host::fp8_gemm_simt(a, stream)
+                 : a.m <= 32                       ? gptq_host::fp8_skinny(a, stream)
                  : gptq_host::fp8_wide_cost(a) < gptq_host::fp8_thin_cost(a)
                      ? gptq_host::fp8_gemm_wide(a, stream)
                      : gptq_host::fp8_thin(a, stream);

@@ -25,6 +25,7 @@ using gptq::fma2;
 using gptq::hi2;
 using gptq::lo2;
 using gptq::pack2;
+using Scales = gptq::ScaleRing<128>;
 using gptq::bar_wait;
 using gptq::bar_wait_rest;
 
@@ -41,7 +42,7 @@ constexpr int REGS_LOAD = 56, REGS_EPI = 224;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP = 8;                     // tile rows per band of the tile order
 constexpr int STAGE_OUT = 4096;              // staging of one epilogue warp's stores
-constexpr int DATA = STAGES * STAGE_BYTES + N_EPI * STAGE_OUT + gptq::ScaleRing::BYTES;
+constexpr int DATA = STAGES * STAGE_BYTES + N_EPI * STAGE_OUT + Scales::BYTES;
 constexpr int SMEM = DATA + 512 + 1024;      // barriers, alignment
 static_assert(SMEM <= 232448 && REGS_LOAD * 128 + REGS_EPI * 256 <= 168 * THREADS, "limits");
 constexpr uint32_t IDESC = gptq::instr_desc(/*e4m3*/ 0, 0, 0, 2 * BM, 2 * BB);
@@ -179,7 +180,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   const uint32_t out_stage = smem + STAGES * STAGE_BYTES;
   // the gated pair stages 64 bytes a row; behind them the rows' maxima, [2 tiles][2 halves][BM]
   const uint32_t amax = out_stage + N_EPI * STAGE_OUT / 2;
-  gptq::ScaleRing scales;
+  Scales scales;
   scales.buf = out_stage + N_EPI * STAGE_OUT;
   const uint32_t bars = smem + DATA;
   auto full = [&](int s) { return bars + (uint32_t)s * 8; };          // used in the first CTA
@@ -189,14 +190,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   auto halves = [&](int q) { return bars + (uint32_t)(2 * STAGES + 2 * NBUF + q) * 8; };
   const uint32_t mma_drain = bars + (2 * STAGES + 2 * NBUF + 4) * 8;
   scales.bars = mma_drain + 8;
-  const uint32_t tmem_slot = scales.bars + gptq::ScaleRing::BAR_BYTES;
+  const uint32_t tmem_slot = scales.bars + Scales::BAR_BYTES;
   const uint32_t abort_flag = tmem_slot + 4, skip_flag = tmem_slot + 8;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t rank;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
 
+  gptq::let_next_kernel_start();
   if (threadIdx.x == 0) {
-    gptq::flag_write(skip_flag, rank == 0 && gptq::status_bad(args.status) ? 1 : 0);
     gptq::flag_write(abort_flag, 0);
     for (int s = 0; s < STAGES; ++s) {
       gptq::bar_init(full(s), 1);
@@ -220,6 +221,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  gptq::wait_for_previous_kernel();
+  if (threadIdx.x == 0)
+    gptq::flag_write(skip_flag, rank == 0 && gptq::status_bad(args.status) ? 1 : 0);
   gptq::tc_fence_before();
   gptq::cluster_sync();  // both CTAs' barriers are set up before either is signalled
   gptq::tc_fence_after();
@@ -319,7 +323,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                             GATED ? args.sw[1] + b0 * args.ldsw[1] : args.sw[0] + b1 * args.ldsw[0],
                             0, nkb, chunk, phase, abort_flag);
       }
-      gptq::ScaleRing::drain();
+      Scales::drain();
     }
   } else {
     gptq::regs_inc<REGS_EPI>();
@@ -345,7 +349,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 32; ++e) acc[c][e] = 0ull;
         for (int kb = 0; kb < nkb; ++kb) {
-          const int j = kb % gptq::ScaleRing::KC;
+          const int j = kb % Scales::KC;
           if (j == 0 && !bar_wait(scales.full(chunk), chunk_phase, abort_flag)) {
             ok = false;
             break;
@@ -355,10 +359,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
           uint64_t f[2];
           f[0] = gptq::pair2(sx * (GATED ? sw.x : half ? sw.y : sw.x));
           f[1] = GATED ? gptq::pair2(sx * sw.y) : f[0];
-          if (j == gptq::ScaleRing::KC - 1 || kb == nkb - 1) {
+          if (j == Scales::KC - 1 || kb == nkb - 1) {
             __syncwarp();
             if (lane == 0) gptq::bar_arrive(scales.empty(chunk));
-            if (++chunk == gptq::ScaleRing::CHUNKS) { chunk = 0; chunk_phase ^= 1; }
+            if (++chunk == Scales::CHUNKS) { chunk = 0; chunk_phase ^= 1; }
           }
           if (!bar_wait_rest(acc_ready, acc_full(buf), acc_phase, abort_flag)) {
             ok = false;
@@ -493,26 +497,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   if (threadIdx.x == 0 && gptq::flag_read(abort_flag)) gptq::set_status(args.status, GPTQ_ERR_TIMEOUT, 5);
 }
 
-template <bool GATED>
-int launch(const CUtensorMap& tx, const CUtensorMap& tw0, const CUtensorMap& tw1, const TcArgs& a,
-           int grid, cudaStream_t stream) {
-  auto kernel = fp8_gemm_kernel<GATED>;
-  if (gptq_host::ensure_smem_attr(reinterpret_cast<const void*>(kernel), SMEM) != 0)
-    return GPTQ_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tx, tw0, tw1, a) == cudaSuccess ? 0 : GPTQ_ERR_CUDA;
-}
-
 }  // namespace
 
 namespace gptq_host {
@@ -565,8 +549,8 @@ int fp8_gemm_wide(const Fp8Gemm& g, cudaStream_t stream) {
     return GPTQ_ERR_CUDA;
   const int pairs = num_sms() / 2;
   const int grid = 2 * (a.n_tiles < pairs ? a.n_tiles : pairs);
-  return gated ? launch<true>(tx, tw0, tw1, a, grid, stream)
-               : launch<false>(tx, tw0, tw1, a, grid, stream);
+  return gated ? fp8_launch(fp8_gemm_kernel<true>, grid, THREADS, SMEM, 2, stream, tx, tw0, tw1, a)
+               : fp8_launch(fp8_gemm_kernel<false>, grid, THREADS, SMEM, 2, stream, tx, tw0, tw1, a);
 }
 
 }  // namespace gptq_host

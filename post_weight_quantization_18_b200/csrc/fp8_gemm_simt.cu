@@ -22,6 +22,8 @@ __global__ void __launch_bounds__(256) fp8_gemm_simt_kernel(SimtArgs a) {
   constexpr int NW = GATED ? 2 : 1;
   __shared__ float xs[TM][TK + 4];
   __shared__ __align__(16) uint8_t ws[NW][TN * W_PITCH];
+  gptq::let_next_kernel_start();
+  gptq::wait_for_previous_kernel();
   if (gptq::status_bad(a.g.status)) return;
   const int tm = blockIdx.x / a.tiles_n, tn = blockIdx.x % a.tiles_n;
   const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
@@ -110,12 +112,8 @@ int fp8_gemm_simt(const Fp8Gemm& g, cudaStream_t stream) {
   a.g = g;
   a.tiles_n = (g.n + TN - 1) / TN;
   const long long ctas = (long long)((g.m + TM - 1) / TM) * a.tiles_n;
-  if (ctas > 0x7FFFFFFFll) return GPTQ_ERR_CUDA;
-  if (g.w[1] != nullptr)
-    fp8_gemm_simt_kernel<true><<<(unsigned)ctas, 256, 0, stream>>>(a);
-  else
-    fp8_gemm_simt_kernel<false><<<(unsigned)ctas, 256, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : GPTQ_ERR_CUDA;
+  return g.w[1] != nullptr ? fp8_launch(fp8_gemm_simt_kernel<true>, ctas, 256, 0, 1, stream, a)
+                           : fp8_launch(fp8_gemm_simt_kernel<false>, ctas, 256, 0, 1, stream, a);
 }
 
 }  // namespace gptq_host

@@ -128,6 +128,15 @@ GPTQ_DEV float2 lds_f32x2(uint32_t at) {
   return v;
 }
 
+GPTQ_DEV float4 lds_f32x4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 // One lane of the warp, the same one each time. The loops that issue MMAs and loads are run by
 // whole warps, with only the instructions themselves under this predicate: in a branch of one lane
 // the compiler cannot keep descriptors and addresses in uniform registers, and a block of K
@@ -148,9 +157,11 @@ GPTQ_DEV bool elect_one() {
 // too late, however early within a step they are issued: they queue behind the operand tiles that the ring
 // has in flight (192 KB, 2500 cycles at 8192 x 8192 x 28672). One warp copies the
 // chunks with cp.async, several of them ahead.
+// ROWS (a multiple of 32) is the number of rows a chunk has room for.
+template <int ROWS>
 struct ScaleRing {
   static constexpr int CHUNKS = 4, KC = 8;
-  static constexpr int PITCH = 132;  // floats between blocks of K: a warp's 8 x 4 copies hit 32 banks
+  static constexpr int PITCH = ROWS + 4;  // floats between blocks of K: 8 x 4 copies hit 32 banks
   static constexpr int FLOATS = KC * PITCH + KC * 2;
   static constexpr int BYTES = CHUNKS * FLOATS * 4;
   static constexpr int BAR_BYTES = 2 * CHUNKS * 8;
@@ -192,6 +203,9 @@ struct ScaleRing {
   GPTQ_DEV float row(int chunk, int j, int r) const {
     return lds_f32(buf + (uint32_t)(chunk * FLOATS + j * PITCH + r) * 4);
   }
+  GPTQ_DEV float4 rows4(int chunk, int j, int r) const {  // of rows r .. r + 3, r a multiple of 4
+    return lds_f32x4(buf + (uint32_t)(chunk * FLOATS + j * PITCH + r) * 4);
+  }
   GPTQ_DEV float2 blocks(int chunk, int j) const {
     return lds_f32x2(buf + (uint32_t)(chunk * FLOATS + KC * PITCH + j * 2) * 4);
   }
@@ -207,6 +221,12 @@ GPTQ_DEV uint64_t pair2(float f) {
   uint64_t r;
   const uint32_t b = __float_as_uint(f);
   asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(b));
+  return r;
+}
+GPTQ_DEV uint64_t mul2(float a, float b, uint64_t f2) {  // (a, b) * f
+  uint64_t v, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v), "l"(f2));
   return r;
 }
 GPTQ_DEV float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
@@ -244,6 +264,48 @@ GPTQ_DEV uint32_t pack2(float a, float b, int dtype) {
   }
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four consecutive columns of an output row from their sums: v[0] as it is in the type of Y (NW = 1),
+// or h = silu(v[0]) v[1] in the format (NW = 2), where the whole warp holds the row's 128 columns
+// of one scale, which goes to sy. vec: Y's rows are 16-byte aligned. row_at: element offset of the
+// row; columns from n on do not exist.
+template <int NW>
+GPTQ_DEV void store_row4(const float4 (&v)[NW], void* y, long long row_at, int col, int n,
+                         int y_dtype, bool vec, float* sy) {
+  float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+  vec = vec && col + 4 <= n;
+  if constexpr (NW == 2) {
+    const float u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t mx = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o[e] = silu_mul(o[e], u[e]);
+      if (col + e < n) mx = max(mx, mag_bits(o[e]));
+    }
+    float s, inv;
+    block_scale(__reduce_max_sync(0xFFFFFFFFu, mx), s, inv);
+    if ((threadIdx.x & 31) == 0) *sy = s;
+    const uint32_t q = e4m3x4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    uint8_t* p = reinterpret_cast<uint8_t*>(y) + row_at + col;
+    if (vec) {
+      *reinterpret_cast<uint32_t*>(p) = q;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < n) p[e] = (uint8_t)(q >> (e * 8));
+    }
+  } else if (vec) {
+    if (y_dtype == GPTQ_F32)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(y) + row_at + col) = v[0];
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(y) + row_at + col) =
+          make_uint2(pack2(o[0], o[1], y_dtype), pack2(o[2], o[3], y_dtype));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < n) store_out(y, row_at + col + e, o[e], y_dtype);
+  }
 }
 
 }  // namespace gptq

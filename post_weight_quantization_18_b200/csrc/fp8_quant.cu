@@ -32,6 +32,8 @@ __global__ void __launch_bounds__(kRowsThreads)
 quantize_rows_kernel(const T* __restrict__ X, long long ldx, long long tiles, int tiles_row, int k,
                      uint8_t* __restrict__ Q, long long ldq, float* __restrict__ S, long long lds,
                      bool vec_x, bool vec_q) {
+  gptq::let_next_kernel_start();
+  gptq::wait_for_previous_kernel();
   const long long tile = (long long)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
   if (tile >= tiles) return;
   const int lane = threadIdx.x & 31;
@@ -78,6 +80,8 @@ quantize_blocks_kernel(const T* __restrict__ X, long long ldx, int m, int k, int
                        uint8_t* __restrict__ Q, long long ldq, float* __restrict__ S,
                        long long lds, bool vec_x, bool vec_q) {
   __shared__ uint32_t part[8];
+  gptq::let_next_kernel_start();
+  gptq::wait_for_previous_kernel();
   const int br = blockIdx.x / groups, g = blockIdx.x % groups;
   const int i0 = threadIdx.x >> 4, c = g * 128 + (threadIdx.x & 15) * 8;
   const int valid = max(0, min(8, k - c));
@@ -175,6 +179,8 @@ __device__ __forceinline__ void finish8(const NormArgs& a, long long row, int c,
 template <typename T, typename TG, int V>
 __global__ void add_rmsnorm_kernel(NormArgs a) {
   __shared__ float part[32];
+  gptq::let_next_kernel_start();
+  gptq::wait_for_previous_kernel();
   const long long row = blockIdx.x;
   float h[V][8];
   float sum = 0.f;
@@ -198,6 +204,8 @@ __global__ void add_rmsnorm_kernel(NormArgs a) {
 template <typename T, typename TG>
 __global__ void __launch_bounds__(1024) add_rmsnorm_wide_kernel(NormArgs a) {
   __shared__ float part[32];
+  gptq::let_next_kernel_start();
+  gptq::wait_for_previous_kernel();
   const long long row = blockIdx.x;
   const int steps = (a.k + 8191) / 8192;  // whole warps in every step
   float sum = 0.f;
@@ -231,11 +239,9 @@ int launch_rows(const void* x, long long ldx, int m, int k, uint8_t* q, long lon
   const int tiles_row = (k + 256 * kRowsUnroll - 1) / (256 * kRowsUnroll);
   const long long tiles = (long long)m * tiles_row;
   const long long ctas = (tiles + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-  if (ctas > 0x7FFFFFFFll) return GPTQ_ERR_CUDA;
-  quantize_rows_kernel<T><<<(unsigned)ctas, kRowsThreads, 0, stream>>>(
-      static_cast<const T*>(x), ldx, tiles, tiles_row, k, q, ldq, s, lds,
-      rows_aligned(x, ldx, sizeof(T), 16), rows_aligned(q, ldq, 1, 8));
-  return cudaGetLastError() == cudaSuccess ? 0 : GPTQ_ERR_CUDA;
+  return gptq_host::fp8_launch(quantize_rows_kernel<T>, ctas, kRowsThreads, 0, 1, stream,
+                               static_cast<const T*>(x), ldx, tiles, tiles_row, k, q, ldq, s, lds,
+                               rows_aligned(x, ldx, sizeof(T), 16), rows_aligned(q, ldq, 1, 8));
 }
 
 template <typename T>
@@ -243,11 +249,9 @@ int launch_blocks(const void* x, long long ldx, int m, int k, uint8_t* q, long l
                   long long lds, cudaStream_t stream) {
   const int groups = (k + 127) / 128;
   const long long ctas = (long long)groups * ((m + 127) / 128);
-  if (ctas > 0x7FFFFFFFll) return GPTQ_ERR_CUDA;
-  quantize_blocks_kernel<T><<<(unsigned)ctas, 256, 0, stream>>>(
-      static_cast<const T*>(x), ldx, m, k, groups, q, ldq, s, lds,
-      rows_aligned(x, ldx, sizeof(T), 16), rows_aligned(q, ldq, 1, 8));
-  return cudaGetLastError() == cudaSuccess ? 0 : GPTQ_ERR_CUDA;
+  return gptq_host::fp8_launch(quantize_blocks_kernel<T>, ctas, 256, 0, 1, stream,
+                               static_cast<const T*>(x), ldx, m, k, groups, q, ldq, s, lds,
+                               rows_aligned(x, ldx, sizeof(T), 16), rows_aligned(q, ldq, 1, 8));
 }
 
 template <typename T, typename TG>
@@ -259,15 +263,14 @@ int launch_norm(NormArgs a, cudaStream_t stream) {
   a.vec_q = rows_aligned(a.q, a.ldq, 1, 8);
   const int vecs = (a.k + 7) / 8;
   auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
+  using gptq_host::fp8_launch;
   if (vecs <= 512)
-    add_rmsnorm_kernel<T, TG, 1><<<a.m, threads(1), 0, stream>>>(a);
-  else if (vecs <= 1024)
-    add_rmsnorm_kernel<T, TG, 2><<<a.m, threads(2), 0, stream>>>(a);
-  else if (vecs <= 2048)
-    add_rmsnorm_kernel<T, TG, 4><<<a.m, threads(4), 0, stream>>>(a);
-  else
-    add_rmsnorm_wide_kernel<T, TG><<<a.m, 1024, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : GPTQ_ERR_CUDA;
+    return fp8_launch(add_rmsnorm_kernel<T, TG, 1>, a.m, threads(1), 0, 1, stream, a);
+  if (vecs <= 1024)
+    return fp8_launch(add_rmsnorm_kernel<T, TG, 2>, a.m, threads(2), 0, 1, stream, a);
+  if (vecs <= 2048)
+    return fp8_launch(add_rmsnorm_kernel<T, TG, 4>, a.m, threads(4), 0, 1, stream, a);
+  return fp8_launch(add_rmsnorm_wide_kernel<T, TG>, a.m, 1024, 0, 1, stream, a);
 }
 
 }  // namespace

@@ -1,0 +1,330 @@
+// fp8_skinny.cu — the products of the e4m3 format for up to 32 rows of activations (decoding), where
+// the time is that of streaming the weight.
+//
+// The operands change places: the 128 rows of a weight block are the M of the MMAs (lanes of tensor
+// memory), the activation rows their N. A thread of the epilogue then owns one weight row and reads
+// one column per activation row, so all lanes work however few rows there are: with the
+// activations as M, one warp in four did, and a gated pair's block of 128 columns took it 2000
+// cycles.
+//
+// A cluster owns the 128 weight rows of a scale block (gated pair: of both weights); its CTAs share
+// out the blocks of K. The sums of a block are scaled by sx sw in fp32 registers as in fp8_gemm.cu.
+// At the end every CTA leaves its sums in shared memory and each row of the output tile is
+// added up over the cluster, always in the same order, by one warp, which for the gated pair
+// also has the whole 128 columns of the row's scale.
+// Two CTAs share an SM, so that one's start and end pass behind the other's stream.
+// Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-7 epilogue (gated pair: 8-11 the
+// second weight's). Every wait is bounded as in fp8_gemm.cu.
+#include "fp8_mma.cuh"
+
+namespace {
+
+using gptq::bar_wait;
+using gptq::bar_wait_rest;
+using Scales = gptq::ScaleRing<32>;
+
+constexpr int BM = 128, BK = 128;
+constexpr int W_TILE = BM * BK;  // 16 KB
+constexpr int NBUF = 4;          // accumulators
+constexpr int PITCH = BM + 4;    // floats of a row of sums
+constexpr int EPI_WARP0 = 4;
+
+template <int NW, int MT>
+struct Cfg {
+  static constexpr int THREADS = 128 + 128 * NW;
+  static constexpr int STAGE_BYTES = NW * W_TILE + MT * BK;
+  static constexpr int STAGES = 104 * 1024 / STAGE_BYTES;  // two CTAs per SM
+  static constexpr int RING = STAGES * STAGE_BYTES;
+  static constexpr int SMEM = RING + Scales::BYTES + 512 + 1024;
+  static constexpr uint32_t TMEM_COLS = NBUF * NW * MT;  // 64, 128 or 256
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024 && STAGES >= 2, "two CTAs per SM");
+  static_assert(NW * MT * PITCH * 4 <= RING, "sums");
+};
+
+struct SkinnyArgs {
+  int M, N, nkb;
+  const float* sx;
+  long long ldsx;
+  const float* sw[2];
+  long long ldsw[2];
+  void* y;
+  long long ldy;
+  float* sy;
+  long long ldsy;
+  int y_dtype;
+  bool y_vec;   // rows of y are 16-byte aligned
+  int ksplit;   // CTAs of a cluster
+  int32_t* status;
+};
+
+template <int NW, int MT>
+__global__ void __launch_bounds__(Cfg<NW, MT>::THREADS, 2)
+fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
+                  const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ SkinnyArgs args) {
+  using C = Cfg<NW, MT>;
+  constexpr uint32_t IDESC = gptq::instr_desc(/*e4m3*/ 0, 0, 0, BM, MT);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem = (gptq::smem_u32(smem_raw) + 1023u) & ~1023u;
+  Scales scales;
+  scales.buf = smem + C::RING;
+  const uint32_t bars = scales.buf + Scales::BYTES;
+  auto full = [&](int s) { return bars + (uint32_t)s * 8; };
+  auto empty = [&](int s) { return bars + (uint32_t)(C::STAGES + s) * 8; };
+  auto acc_full = [&](int b) { return bars + (uint32_t)(2 * C::STAGES + b) * 8; };
+  auto acc_empty = [&](int b) { return bars + (uint32_t)(2 * C::STAGES + NBUF + b) * 8; };
+  const uint32_t mma_drain = bars + (2 * C::STAGES + 2 * NBUF) * 8;
+  scales.bars = mma_drain + 8;
+  const uint32_t tmem_slot = scales.bars + Scales::BAR_BYTES;
+  const uint32_t abort_flag = tmem_slot + 4, skip_flag = tmem_slot + 8;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  uint32_t rank;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+
+  gptq::let_next_kernel_start();
+  if (threadIdx.x == 0) {
+    gptq::flag_write(abort_flag, 0);
+    for (int s = 0; s < C::STAGES; ++s) {
+      gptq::bar_init(full(s), 1);
+      gptq::bar_init(empty(s), 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      gptq::bar_init(acc_full(b), 1);
+      gptq::bar_init(acc_empty(b), 4 * NW);
+    }
+    scales.init(4 * NW);
+    gptq::bar_init(mma_drain, 1);
+    gptq::fence_barrier_init();
+  } else if (threadIdx.x == 32 * 3) {
+    gptq::tma_prefetch_desc(&tmX);
+    gptq::tma_prefetch_desc(&tmW0);
+    if (NW == 2) gptq::tma_prefetch_desc(&tmW1);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_slot),
+                 "r"(C::TMEM_COLS)
+                 : "memory");
+    gptq::tmem_relinquish();
+  }
+  gptq::wait_for_previous_kernel();
+  if (threadIdx.x == 0) gptq::flag_write(skip_flag, gptq::status_bad(args.status) ? 1 : 0);
+  gptq::tc_fence_before();
+  __syncthreads();
+  gptq::tc_fence_after();
+  const uint32_t tmem_base = gptq::flag_read(tmem_slot);
+  const bool skip = gptq::flag_read(skip_flag) != 0;
+  const int block = blockIdx.x / args.ksplit;  // of 128 weight rows
+  const int kb0 = (int)((long long)args.nkb * rank / args.ksplit);
+  const int kb1 = (int)((long long)args.nkb * (rank + 1) / args.ksplit);
+
+  if (warp < EPI_WARP0) {
+    if (skip) {
+    } else if (warp == 0) {  // ---------------- TMA producer ----------------
+      const bool leader = gptq::elect_one();
+      int stage = 0;
+      uint32_t phase = 0, filled = 0, fill_parity = 0;
+      bool ready = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!bar_wait_rest(ready, empty(stage), phase ^ 1, abort_flag)) break;
+        const uint32_t sw = smem + (uint32_t)(stage * C::STAGE_BYTES), here = full(stage);
+        filled |= 1u << stage;
+        fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+        ready = gptq::bar_poll(empty(stage), phase ^ 1);
+        if (leader) {
+          gptq::bar_expect(here, C::STAGE_BYTES);
+          gptq::load_tile_2d(sw, &tmW0, here, kb * BK, block * BM);
+          if (NW == 2) gptq::load_tile_2d(sw + W_TILE, &tmW1, here, kb * BK, block * BM);
+          gptq::load_tile_2d(sw + NW * W_TILE, &tmX, here, kb * BK, 0);
+        }
+        __syncwarp();
+      }
+      if (gptq::flag_read(abort_flag))
+        for (int s = 0; s < C::STAGES; ++s)
+          if (filled & (1u << s)) gptq::bar_drain(full(s), (fill_parity >> s) & 1u);
+    } else if (warp == 1) {  // ---------------- MMA issuer ----------------
+      const bool leader = gptq::elect_one();
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool acc_ready = true, full_ready = false;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!bar_wait_rest(acc_ready, acc_empty(buf), acc_phase ^ 1, abort_flag) ||
+            !bar_wait_rest(full_ready, full(stage), phase, abort_flag))
+          break;
+        gptq::tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(buf * NW * MT);
+        const uint32_t sw = smem + (uint32_t)(stage * C::STAGE_BYTES), sx = sw + NW * W_TILE;
+        const uint32_t freed = empty(stage), filled = acc_full(buf);
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+        if (++buf == NBUF) { buf = 0; acc_phase ^= 1; }
+        full_ready = gptq::bar_poll(full(stage), phase);
+        acc_ready = gptq::bar_poll(acc_empty(buf), acc_phase ^ 1);
+        if (leader) {
+#pragma unroll
+          for (int w = 0; w < NW; ++w)
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)  // 32 columns: 32 bytes along the swizzled rows
+              gptq::mma_f8(d + (uint32_t)(w * MT),
+                           gptq::smem_desc_sw128(sw + w * W_TILE + kk * 32, 16, 1024),
+                           gptq::smem_desc_sw128(sx + kk * 32, 16, 1024), IDESC, kk > 0);
+          gptq::commit_to(freed);
+          gptq::commit_to(filled);
+        }
+        __syncwarp();
+      }
+      if (gptq::flag_read(abort_flag)) {
+        if (leader) gptq::commit_to(mma_drain);
+        __syncwarp();
+        gptq::bar_drain(mma_drain, 0);
+      }
+    } else if (warp == 2) {  // ---------------- scales ----------------
+      int chunk = 0;
+      uint32_t phase = 0;
+      scales.produce(args.sx, args.ldsx, 0, MT, args.M, args.sw[0] + block * args.ldsw[0],
+                     args.sw[NW - 1] + block * args.ldsw[NW - 1], kb0, kb1, chunk, phase,
+                     abort_flag);
+      Scales::drain();
+    }
+    gptq::cluster_sync();
+    gptq::cluster_sync();
+  } else {
+    // ---------------- epilogue: one weight row a thread ----------------
+    const int quarter = warp & 3, w = (warp - EPI_WARP0) >> 2;
+    const uint32_t acc_col = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(w * MT);
+    int buf = 0, chunk = 0;
+    uint32_t acc_phase = 0, chunk_phase = 0;
+    bool ok = !skip, acc_ready = false;
+    uint64_t acc[MT / 2];
+#pragma unroll
+    for (int c = 0; c < MT / 2; ++c) acc[c] = 0ull;
+    for (int kb = kb0; kb < kb1 && ok; ++kb) {
+      const int j = (kb - kb0) % Scales::KC;
+      if ((j == 0 && !bar_wait(scales.full(chunk), chunk_phase, abort_flag)) ||
+          !bar_wait_rest(acc_ready, acc_full(buf), acc_phase, abort_flag)) {
+        ok = false;
+        break;
+      }
+      gptq::tc_fence_after();
+      const float2 sw2 = scales.blocks(chunk, j);
+      const uint64_t sw = gptq::pair2(NW == 2 && w ? sw2.y : sw2.x);
+      uint32_t r[MT / 16][16];
+#pragma unroll
+      for (int c = 0; c < MT / 16; ++c)
+        gptq::tmem_ld_32x32b_x16(acc_col + (uint32_t)(buf * NW * MT + 16 * c), r[c]);
+      gptq::tmem_ld_wait();
+      gptq::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) gptq::bar_arrive(acc_empty(buf));
+      if (++buf == NBUF) { buf = 0; acc_phase ^= 1; }
+      acc_ready = gptq::bar_poll(acc_full(buf), acc_phase);
+#pragma unroll
+      for (int c = 0; c < MT / 16; ++c) {
+        gptq::settled(r[c]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 sx = scales.rows4(chunk, j, 16 * c + 4 * e);
+          uint64_t* a = acc + 8 * c + 2 * e;
+          gptq::fma2(a[0], r[c][4 * e], r[c][4 * e + 1], gptq::mul2(sx.x, sx.y, sw));
+          gptq::fma2(a[1], r[c][4 * e + 2], r[c][4 * e + 3], gptq::mul2(sx.z, sx.w, sw));
+        }
+      }
+      if (j == Scales::KC - 1) {
+        __syncwarp();
+        if (lane == 0) gptq::bar_arrive(scales.empty(chunk));
+        if (++chunk == Scales::CHUNKS) { chunk = 0; chunk_phase ^= 1; }
+      }
+    }
+    // All MMAs of the CTA are done, so the operand ring is free: rows of 128 sums.
+    if (ok) {
+#pragma unroll
+      for (int c = 0; c < MT; ++c)
+        if (c < args.M)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                           smem + (uint32_t)((w * MT + c) * PITCH + quarter * 32 + lane) * 4),
+                       "f"(c & 1 ? gptq::hi2(acc[c / 2]) : gptq::lo2(acc[c / 2]))
+                       : "memory");
+    }
+    // Every thread of every CTA of the cluster passes both barriers, whatever happened above.
+    gptq::cluster_sync();
+    if (!skip) {
+      // Rows are dealt out to the warps of all CTAs in turn.
+      for (int r = (int)rank * 4 * NW + warp - EPI_WARP0; r < args.M; r += args.ksplit * 4 * NW) {
+        float4 v[NW];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          const uint32_t at = smem + (uint32_t)((i * MT + r) * PITCH + lane * 4) * 4;
+          float4 p[8];
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (s < args.ksplit) p[s] = gptq::ld_cluster(at, s);
+          v[i] = p[0];
+#pragma unroll
+          for (int s = 1; s < 8; ++s)
+            if (s < args.ksplit) {
+              v[i].x += p[s].x;
+              v[i].y += p[s].y;
+              v[i].z += p[s].z;
+              v[i].w += p[s].w;
+            }
+        }
+        gptq::store_row4<NW>(v, args.y, (long long)r * args.ldy, block * 128 + lane * 4, args.N,
+                             args.y_dtype, args.y_vec,
+                             args.sy + (NW == 2 ? (long long)r * args.ldsy + block : 0));
+      }
+    }
+    gptq::cluster_sync();  // no CTA leaves while its sums may still be read
+  }
+
+  gptq::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) gptq::tmem_dealloc(tmem_base, C::TMEM_COLS);
+  if (threadIdx.x == 0 && gptq::flag_read(abort_flag))
+    gptq::set_status(args.status, GPTQ_ERR_TIMEOUT, 7);
+}
+
+template <int NW, int MT>
+int launch(const gptq_host::Fp8Gemm& g, const SkinnyArgs& a, int blocks, cudaStream_t stream) {
+  using C = Cfg<NW, MT>;
+  using gptq_host::make_tmap_2d;
+  CUtensorMap tx, tw[2];
+  if (make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.x, (uint64_t)g.k, (uint64_t)g.m,
+                   (uint64_t)g.ldx, BK, MT, CU_TENSOR_MAP_SWIZZLE_128B) != 0)
+    return GPTQ_ERR_CUDA;
+  for (int i = 0; i < NW; ++i)
+    if (make_tmap_2d(&tw[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.w[i], (uint64_t)g.k, (uint64_t)g.n,
+                     (uint64_t)g.ldw[i], BK, BM, CU_TENSOR_MAP_SWIZZLE_128B) != 0)
+      return GPTQ_ERR_CUDA;
+  return gptq_host::fp8_launch(fp8_skinny_kernel<NW, MT>, (long long)blocks * a.ksplit, C::THREADS,
+                               C::SMEM, a.ksplit, stream, tx, tw[0], tw[NW - 1], a);
+}
+
+}  // namespace
+
+namespace gptq_host {
+
+int fp8_skinny(const Fp8Gemm& g, cudaStream_t stream) {
+  const bool gated = g.w[1] != nullptr;
+  SkinnyArgs a{};
+  a.M = g.m; a.N = g.n;
+  a.nkb = (g.k + BK - 1) / BK;
+  a.sx = g.sx; a.ldsx = g.ldsx;
+  for (int i = 0; i < 2; ++i) {
+    a.sw[i] = g.sw[i];
+    a.ldsw[i] = g.ldsw[i];
+  }
+  a.y = g.y; a.ldy = g.ldy; a.y_dtype = g.y_dtype;
+  a.sy = g.sy; a.ldsy = g.ldsy;
+  a.status = g.status;
+  const int es = gated ? 1 : g.y_dtype == GPTQ_F32 ? 4 : 2;
+  a.y_vec = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.ldy * es % 16 == 0;
+  const int blocks = (g.n + BM - 1) / BM;
+  // As many CTAs along K as the SMs hold two of, each with four blocks of K at least.
+  const int sms = num_sms();
+  a.ksplit = 1;
+  while (a.ksplit < 8 && blocks * (a.ksplit + 1) <= 2 * sms && a.nkb >= 4 * (a.ksplit + 1))
+    ++a.ksplit;
+  if (gated)
+    return g.m <= 16 ? launch<2, 16>(g, a, blocks, stream) : launch<2, 32>(g, a, blocks, stream);
+  return g.m <= 16 ? launch<1, 16>(g, a, blocks, stream) : launch<1, 32>(g, a, blocks, stream);
+}
+
+}  // namespace gptq_host

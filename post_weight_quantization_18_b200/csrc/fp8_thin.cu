@@ -25,6 +25,7 @@ namespace {
 using gptq::fma2;
 using gptq::hi2;
 using gptq::lo2;
+using Scales = gptq::ScaleRing<128>;
 using gptq::bar_wait;
 using gptq::bar_wait_rest;
 
@@ -32,7 +33,7 @@ constexpr int BM = 128, BK = 128;
 constexpr int THREADS = 384, EPI_WARP0 = 4, N_EPI = 8;
 constexpr int RING_BYTES = 196 * 1024;   // operand ring
 constexpr int MAX_STAGES = 8;
-constexpr int SMEM_BYTES = RING_BYTES + gptq::ScaleRing::BYTES + 4 * BM * 4 + 512 + 1024;
+constexpr int SMEM_BYTES = RING_BYTES + Scales::BYTES + 4 * BM * 4 + 512 + 1024;
 constexpr uint32_t TMEM_COLS = 512;
 
 struct ThinArgs {
@@ -73,9 +74,9 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   constexpr uint32_t IDESC = gptq::instr_desc(/*e4m3*/ 0, 0, 0, BM, BN);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (gptq::smem_u32(smem_raw) + 1023u) & ~1023u;
-  gptq::ScaleRing scales;
+  Scales scales;
   scales.buf = smem + RING_BYTES;
-  const uint32_t amax = scales.buf + gptq::ScaleRing::BYTES;  // [2 tiles][2 halves][BM]
+  const uint32_t amax = scales.buf + Scales::BYTES;  // [2 tiles][2 halves][BM]
   const uint32_t bars = amax + 4 * BM * 4;
   auto full = [&](int s) { return bars + (uint32_t)s * 8; };
   auto empty = [&](int s) { return bars + (uint32_t)(MAX_STAGES + s) * 8; };
@@ -84,12 +85,12 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   auto halves = [&](int q) { return bars + (uint32_t)(2 * MAX_STAGES + 4 + q) * 8; };
   const uint32_t mma_drain = bars + (2 * MAX_STAGES + 8) * 8;
   scales.bars = mma_drain + 8;
-  const uint32_t tmem_slot = scales.bars + gptq::ScaleRing::BAR_BYTES;
+  const uint32_t tmem_slot = scales.bars + Scales::BAR_BYTES;
   const uint32_t abort_flag = tmem_slot + 4, skip_flag = tmem_slot + 8;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  gptq::let_next_kernel_start();
   if (threadIdx.x == 0) {
-    gptq::flag_write(skip_flag, gptq::status_bad(args.status) ? 1 : 0);
     gptq::flag_write(abort_flag, 0);
     for (int s = 0; s < MAX_STAGES; ++s) {
       gptq::bar_init(full(s), 1);
@@ -114,6 +115,8 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
                  : "memory");
     gptq::tmem_relinquish();
   }
+  gptq::wait_for_previous_kernel();
+  if (threadIdx.x == 0) gptq::flag_write(skip_flag, gptq::status_bad(args.status) ? 1 : 0);
   gptq::tc_fence_before();
   __syncthreads();
   gptq::tc_fence_after();
@@ -243,7 +246,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
                                     : args.sw[0] + b1 * args.ldsw[0],
                             kb0, kb1, chunk, phase, abort_flag);
       }
-      gptq::ScaleRing::drain();
+      Scales::drain();
     }
     if constexpr (CLUSTERED) {
       gptq::cluster_sync();
@@ -272,7 +275,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[w][c][e] = 0ull;
       for (int kb = kb0; kb < kb1; kb += KPS) {
-        const int nb = min(KPS, kb1 - kb), j = (kb - kb0) % gptq::ScaleRing::KC;
+        const int nb = min(KPS, kb1 - kb), j = (kb - kb0) % Scales::KC;
         if (j == 0 && !bar_wait(scales.full(chunk), chunk_phase, abort_flag)) {
           ok = false;
           break;
@@ -287,10 +290,10 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
             if (NW == 2 || TWO_BLOCKS) f[b][1] = gptq::pair2(sx * sw.y);
           }
         }
-        if (j + KPS == gptq::ScaleRing::KC || kb + KPS >= kb1) {
+        if (j + KPS == Scales::KC || kb + KPS >= kb1) {
           __syncwarp();
           if (lane == 0) gptq::bar_arrive(scales.empty(chunk));
-          if (++chunk == gptq::ScaleRing::CHUNKS) { chunk = 0; chunk_phase ^= 1; }
+          if (++chunk == Scales::CHUNKS) { chunk = 0; chunk_phase ^= 1; }
         }
         if (!bar_wait(acc_full(buf), acc_phase, abort_flag)) {
           ok = false;
@@ -461,43 +464,11 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
                 v[w].w += p[s].w;
               }
           }
-          const long long row = row_tile(t0) * BM + r;
-          const int col = tile_col + c4;
-          float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-          if constexpr (NW == 2) {
-            const float u[4] = {v[NW - 1].x, v[NW - 1].y, v[NW - 1].z, v[NW - 1].w};
-            uint32_t mx = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[e] = gptq::silu_mul(o[e], u[e]);
-              if (col + e < args.N) mx = max(mx, gptq::mag_bits(o[e]));
-            }
-            float s, inv;
-            gptq::block_scale(__reduce_max_sync(0xFFFFFFFFu, mx), s, inv);
-            if (lane == 0) args.sy[row * args.ldsy + tile_col / 128] = s;
-            const uint32_t q = gptq::e4m3x4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-            uint8_t* p = reinterpret_cast<uint8_t*>(args.y) + row * args.ldy + col;
-            if (args.y_vec && col + 4 <= args.N) {
-              *reinterpret_cast<uint32_t*>(p) = q;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (col + e < args.N) p[e] = (uint8_t)(q >> (e * 8));
-            }
-          } else if (live) {
-            const long long at = row * args.ldy + col;
-            if (args.y_vec && col + 4 <= args.N) {
-              if (args.y_dtype == GPTQ_F32)
-                *reinterpret_cast<float4*>(reinterpret_cast<float*>(args.y) + at) = v[0];
-              else
-                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(args.y) + at) =
-                    make_uint2(gptq::pack2(o[0], o[1], args.y_dtype),
-                               gptq::pack2(o[2], o[3], args.y_dtype));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (col + e < args.N) gptq::store_out(args.y, at + e, o[e], args.y_dtype);
-            }
+          if (live) {
+            const long long row = row_tile(t0) * BM + r;
+            gptq::store_row4<NW>(v, args.y, row * args.ldy, tile_col + c4, args.N, args.y_dtype,
+                                 args.y_vec,
+                                 args.sy + (NW == 2 ? row * args.ldsy + tile_col / 128 : 0));
           }
         }
       }
@@ -553,22 +524,10 @@ int launch(const gptq_host::Fp8Gemm& g, ThinArgs a, int sms, cudaStream_t stream
   } else {
     maps.w1[0] = maps.w1[1] = maps.w0[0];
   }
-  auto kernel = fp8_thin_kernel<NW, CH, CLUSTERED>;
-  if (gptq_host::ensure_smem_attr(reinterpret_cast<const void*>(kernel), SMEM_BYTES) != 0)
-    return GPTQ_ERR_CUDA;
   const int csize = CLUSTERED ? CN * a.ksplit : 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(CLUSTERED ? a.n_tiles * csize : a.n_tiles < sms ? a.n_tiles : sms));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)csize;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = CLUSTERED ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? 0 : GPTQ_ERR_CUDA;
+  const int grid = CLUSTERED ? a.n_tiles * csize : a.n_tiles < sms ? a.n_tiles : sms;
+  return gptq_host::fp8_launch(fp8_thin_kernel<NW, CH, CLUSTERED>, grid, THREADS, SMEM_BYTES, csize,
+                               stream, maps, a);
 }
 
 }  // namespace
