@@ -7,11 +7,11 @@
 
 #include "../../include/fp8.h"
 #include "common.cuh"
+#include "fp8_scale.cuh"
 
 namespace gptq {
 
 constexpr int kFp8Block = 128;           // columns (and weight rows) that share one scale
-constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: 1 / s stays finite
 
 // The kernels here are launched so that one may start while the kernel before it in the stream still
@@ -51,7 +51,7 @@ GPTQ_DEV void block_scale(uint32_t amax_bits, float& s, float& inv) {
   } else if (amax_bits == 0u) {
     s = inv = 1.f;
   } else {
-    s = fmaxf(__fdiv_rn(__uint_as_float(amax_bits), kE4m3Max), kMinScale);
+    s = fmaxf(div_e4m3_max(__uint_as_float(amax_bits)), kMinScale);
     inv = __frcp_rn(s);
   }
 }
@@ -97,6 +97,52 @@ struct Vec8 {
     }
   }
 };
+
+template <typename T>
+GPTQ_DEV Vec8<T> pack8(const float (&f)[8]) {
+  Vec8<T> v;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.w[i] = __float_as_uint(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        v.w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      } else {
+        const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        v.w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+    }
+  }
+  return v;
+}
+
+// The larger magnitude, NaN if either is NaN; the sign means nothing.
+GPTQ_DEV float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The largest magnitude of the eight, as mag_bits of it. 16-bit types are compared as they are: without
+// the sign their bits are ordered like the values, infinities and NaNs on top.
+template <typename T>
+GPTQ_DEV uint32_t max_mag(const Vec8<T>& v) {
+  if constexpr (sizeof(T) == 4) {
+    float m = v.get(0);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_abs(m, v.get(i));
+    return mag_bits(m);
+  } else {
+    uint32_t m = v.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __vmaxu2(m, v.w[i] & 0x7FFF7FFFu);
+    const uint16_t h = (uint16_t)max(m >> 16, m & 0xFFFFu);
+    return __float_as_uint(to_f32<T>(*reinterpret_cast<const T*>(&h)));
+  }
+}
 
 // `valid` (0..8) elements at p, zeros behind them. vec: p is 16-byte aligned.
 template <typename T>
