@@ -8,14 +8,18 @@
 Each .cu under csrc/ is compiled to an object (in parallel) and the objects are linked into one
 shared library next to this file. The CUDA runtime is linked statically; the driver API is
 reached through cudaGetDriverEntryPoint, so libcuda is not a link-time dependency.
+csrc/fp8_binding.cpp is compiled against the Python and torch headers into _fp8_binding.so, the
+extension module that calls the library's 8-bit floating point operators.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +27,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgptq_b200.so")
+BINDING = os.path.join(HERE, "_fp8_binding.so")
+BINDING_SRC = os.path.join(CSRC, "fp8_binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -52,7 +58,40 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(p) <= t
+               for p in [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
+def build_binding() -> None:
+    """_fp8_binding.so from csrc/fp8_binding.cpp (the library has to be there: it is linked)."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_library(force, verbose)
+    if force or not binding_up_to_date():
+        build_binding()
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

@@ -233,6 +233,8 @@ __device__ __forceinline__ float inv_rms(float sum, const NormArgs& a) {
 template <typename T, typename TG, int V, bool TEAM_WARP>
 __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   constexpr bool AHEAD = sizeof(T) == 2;
+  // gamma before the row's sum, but not where a CTA has one row only and the registers are short
+  constexpr bool EARLY = AHEAD || V == 1;
   extern __shared__ __align__(16) uint8_t next_row[];  // [x, r][V][threads] of 16 bytes
   __shared__ float part[2][32];
   gptq::let_next_kernel_start();
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const __grid_constant_
   Vec8<TG> gamma[V];
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (AHEAD) gamma[v] = load_gamma(v);
+    if (EARLY) gamma[v] = load_gamma(v);
   int flip = 0;
   for (long long row = row0; row < a.m; row += stride) {
     float h[V][8];
@@ -297,8 +299,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const __grid_constant_
     fetch(row + stride);  // into the place just read
     sum = TEAM_WARP ? warp_sum(sum) : block_sum(sum, part[flip]);
     flip ^= 1;
-    // one row a CTA: no registers for gamma during the sum
-    finish<T, V>(a, row, c0, step, h, [&](int v) { return AHEAD ? gamma[v] : load_gamma(v); },
+    finish<T, V>(a, row, c0, step, h, [&](int v) { return EARLY ? gamma[v] : load_gamma(v); },
                  inv_rms(sum, a));
   }
 }
