@@ -69,6 +69,9 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   constexpr int CN = NW == 2 ? 128 / BN : 1;                    // CTAs along the columns of a scale
   constexpr bool TWO_BLOCKS = 128 % BN != 0;                    // a tile may span two weight blocks
   constexpr int PITCH = BN + 4;                                 // floats; an odd number of 16 bytes
+  // 128 sums a thread: the first warpgroup's registers go to the epilogue's, 128 * 56 + 256 * 224 =
+  // 384 * 168 as in fp8_gemm.cu
+  constexpr bool SPLIT_REGS = NW * CH == 8;
   static_assert(NW == 1 || CN * BN == 128, "the gated pair's tiles divide a scale's columns");
   static_assert(NW * BM * PITCH * 4 <= RING_BYTES, "partial sums");
   constexpr uint32_t IDESC = gptq::instr_desc(/*e4m3*/ 0, 0, 0, BM, BN);
@@ -141,6 +144,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   auto col_of = [&](int t) { return (t % args.tiles_n) * (CN * BN) + npart * BN; };
 
   if (warp < EPI_WARP0) {
+    if constexpr (SPLIT_REGS) gptq::regs_dec<56>();
     if (gptq::flag_read(skip_flag)) {
     } else if (warp == 0) {  // ---------------- TMA producer ----------------
       const bool leader = gptq::elect_one();
@@ -254,12 +258,13 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
     }
   } else {
     // ---------------- epilogue ----------------
+    if constexpr (SPLIT_REGS) gptq::regs_inc<224>();
     const int quarter = warp & 3, half = (warp - EPI_WARP0) >> 2;
     const uint32_t lane_field = (uint32_t)(quarter * 32) << 16;
     constexpr int HC = BN / 2;  // columns of a thread, per weight: CH chunks of 16
     int buf = 0, chunk = 0;
     uint32_t acc_phase = 0, tile_parity = 0, chunk_phase = 0;
-    bool ok = !gptq::flag_read(skip_flag);
+    bool ok = !gptq::flag_read(skip_flag), acc_ready = false;
     for (int t = t0; t < args.n_tiles && ok; t += step) {
       const int row0 = row_tile(t) * BM + quarter * 32, row = row0 + lane;
       const int col0 = col_of(t) + half * HC;
@@ -295,42 +300,60 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
           if (lane == 0) gptq::bar_arrive(scales.empty(chunk));
           if (++chunk == Scales::CHUNKS) { chunk = 0; chunk_phase ^= 1; }
         }
-        if (!bar_wait(acc_full(buf), acc_phase, abort_flag)) {
+        if (!bar_wait_rest(acc_ready, acc_full(buf), acc_phase, abort_flag)) {
           ok = false;
           break;
         }
         gptq::tc_fence_after();
-        if (rows_here) {
-#pragma unroll
-          for (int b = 0; b < KPS; ++b) {
-            if (b >= nb) break;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-              uint32_t r[CH][16];
-              __syncwarp();
-#pragma unroll
-              for (int c = 0; c < CH; ++c)
-                gptq::tmem_ld_32x32b_x16(tmem_base + lane_field +
-                                             (uint32_t)((buf * KPS + b) * COLS + w * BN +
-                                                        half * HC + 16 * c),
-                                         r[c]);
-              gptq::tmem_ld_wait();
-#pragma unroll
-              for (int c = 0; c < CH; ++c) {
-                gptq::settled(r[c]);
-                uint64_t fc = f[b][w];
-                if constexpr (TWO_BLOCKS) fc = c < cut ? f[b][0] : f[b][1];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  fma2(acc[w][c][e], r[c][2 * e], r[c][2 * e + 1], fc);
-              }
-            }
-          }
-        }
-        gptq::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) gptq::bar_arrive(acc_empty(buf));
+        const uint32_t acc_col =
+            tmem_base + lane_field + (uint32_t)(buf * KPS * COLS + half * HC);
+        const uint32_t freed = acc_empty(buf);
         if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+        // The group's chunks of 16 columns, four loads at a time; chunk i is of block i / (NW CH).
+        constexpr int CHUNKS = KPS * NW * CH;
+        auto column = [&](int i) {
+          return acc_col + (uint32_t)(i / (NW * CH) * COLS + i / CH % NW * BN + i % CH * 16);
+        };
+        auto add = [&](int i, uint32_t(&r)[16]) {
+          const int b = i / (NW * CH), w = i / CH % NW, c = i % CH;
+          uint64_t fc = f[b][w];
+          if constexpr (TWO_BLOCKS) fc = c < cut ? f[b][0] : f[b][1];
+          gptq::settled(r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) fma2(acc[w][c][e], r[2 * e], r[2 * e + 1], fc);
+        };
+        auto release = [&] {  // all of it is in registers: the accumulators are free
+          gptq::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) gptq::bar_arrive(freed);
+          acc_ready = gptq::bar_poll(acc_full(buf), acc_phase);
+        };
+        if (!rows_here) {
+          release();
+        } else if (nb == KPS) {
+#pragma unroll
+          for (int i = 0; i < CHUNKS; i += 4) {
+            uint32_t r[4][16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (i + j < CHUNKS) gptq::tmem_ld_32x32b_x16(column(i + j), r[j]);
+            gptq::tmem_ld_wait();
+            if (i + 4 >= CHUNKS) release();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (i + j < CHUNKS) add(i + j, r[j]);
+          }
+        } else {  // the last blocks of K: accumulators behind them hold something else
+#pragma unroll
+          for (int i = 0; i < CHUNKS; ++i)
+            if (i / (NW * CH) < nb) {
+              uint32_t r[16];
+              gptq::tmem_ld_32x32b_x16(column(i), r);
+              gptq::tmem_ld_wait();
+              add(i, r);
+            }
+          release();
+        }
       }
       if (!ok) break;
       if constexpr (CLUSTERED) {
