@@ -232,6 +232,10 @@ int fp8_launch(void (*kernel)(P...), long long grid, int threads, int smem, int 
                                                                                   : GPTQ_ERR_CUDA;
 }
 
+// Clusters of `size` CTAs (2 to 8) of so many threads and bytes of shared memory that the current device
+// holds at once; worked out once for each.
+int resident_clusters(int threads, int smem, int size);
+
 struct Fp8Gemm {  // arguments of one product, or of the gated pair (w1 != nullptr)
   const uint8_t* x;
   long long ldx;
@@ -249,6 +253,12 @@ struct Fp8Gemm {  // arguments of one product, or of the gated pair (w1 != nullp
   long long ldsy;
   int32_t* status;
 };
+
+// The alignment in bytes (16, 8, 4, 2 or 1) that every row of a matrix has.
+inline int row_align(const void* p, long long pitch_bytes) {
+  const unsigned long long bits = reinterpret_cast<uintptr_t>(p) | (unsigned long long)pitch_bytes | 16;
+  return (int)(bits & (0 - bits));
+}
 
 int fp8_quantize_rows(const void* x, int dtype, long long ldx, int m, int k, uint8_t* q,
                       long long ldq, float* s, long long lds, cudaStream_t stream);

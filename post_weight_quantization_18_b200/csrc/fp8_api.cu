@@ -2,6 +2,8 @@
 // host, then one kernel launch each.
 #include <math.h>
 
+#include <mutex>
+
 #include "fp8.cuh"
 
 namespace {
@@ -30,6 +32,50 @@ int gemm_launch(const gptq_host::Fp8Gemm& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+namespace {
+
+// Never launched: a kernel for the occupancy calculator, which counts one CTA an SM for kernels that
+// allocate tensor memory, however little (two of the streaming kernel's run together).
+__global__ void __launch_bounds__(384) occupancy_kernel() {}
+
+}  // namespace
+
+namespace gptq_host {
+
+int resident_clusters(int threads, int smem, int size) {
+  struct Entry { int threads, smem, dev, size, count; };
+  static Entry known[64];
+  static int n_known = 0;
+  static std::mutex mu;
+  int dev = 0;
+  if (size < 2 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < n_known; ++i)
+    if (known[i].threads == threads && known[i].smem == smem && known[i].dev == dev &&
+        known[i].size == size)
+      return known[i].count;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int count = 0;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(occupancy_kernel), smem) != 0 ||
+      cudaOccupancyMaxActiveClusters(&count, occupancy_kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    count = 0;
+  }
+  if (n_known < 64) known[n_known++] = Entry{threads, smem, dev, size, count};
+  return count;
+}
+
+}  // namespace gptq_host
 
 extern "C" {
 

@@ -58,7 +58,7 @@ struct TcArgs {
   float* sy;
   long long ldsy;
   int y_dtype;
-  bool y_vec;   // rows of y are 16-byte aligned
+  int y_align;  // of the rows of y, in bytes
   int tiles_m, tiles_n, n_tiles;
   int32_t* status;
 };
@@ -142,29 +142,41 @@ template <int ES>
 __device__ __forceinline__ void flush_rows(const TcArgs& a, uint32_t st, int row0, int col0,
                                            int lane) {
   constexpr int PER = 16 / ES;  // elements of a piece
-  const int piece = lane & 7;
-  const int col = col0 + piece * PER;
   __syncwarp();
+  if (a.y_align == 16) {
+    const int piece = lane & 7, col = col0 + piece * PER;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 4 + (lane >> 3);
-    const uint4 v = lds16(staged(st, r, piece));
-    if (row0 + r < a.M && col < a.N) {
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      const uint4 v = lds16(staged(st, r, piece));
+      if (row0 + r < a.M && col < a.N) {
+        uint8_t* p = reinterpret_cast<uint8_t*>(a.y) + ((long long)(row0 + r) * a.ldy + col) * ES;
+        if (col + PER <= a.N) {
+          *reinterpret_cast<uint4*>(p) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < PER; ++e)
+            if (col + e < a.N) {
+              if constexpr (ES == 4)
+                reinterpret_cast<uint32_t*>(p)[e] = w[e];
+              else
+                reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
+            }
+        }
+      }
+    }
+  } else {  // a row at a time, one word a lane, so that the warp's stores are neighbours all the same
+    const int col = col0 + lane * (4 / ES);
+    for (int r = 0; r < 32 && row0 + r < a.M; ++r) {
+      const uint32_t w = gptq::flag_read(staged(st, r, lane >> 2) + (lane & 3) * 4);
       uint8_t* p = reinterpret_cast<uint8_t*>(a.y) + ((long long)(row0 + r) * a.ldy + col) * ES;
-      if (a.y_vec && col + PER <= a.N) {
-        *reinterpret_cast<uint4*>(p) = v;
+      if (ES == 4 || (a.y_align >= 4 && col + 1 < a.N)) {
+        if (col < a.N) *reinterpret_cast<uint32_t*>(p) = w;
       } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < PER; ++e)
-          if (col + e < a.N) {
-            if constexpr (ES == 4)
-              reinterpret_cast<uint32_t*>(p)[e] = w[e];
-            else if constexpr (ES == 2)
-              reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
-            else
-              p[e] = (uint8_t)(w[e >> 2] >> ((e & 3) * 8));
-          }
+        for (int e = 0; e < 2; ++e)
+          if (col + e < a.N) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w >> (e * 16));
       }
     }
   }
@@ -436,7 +448,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             const uint4 v = lds16(staged64(st, r, piece));
             if (row0 + r < args.M && col < args.N) {
               uint8_t* p = reinterpret_cast<uint8_t*>(args.y) + (long long)(row0 + r) * args.ldy + col;
-              if (args.y_vec && col + 16 <= args.N) {
+              if (args.y_align == 16 && col + 16 <= args.N) {
                 *reinterpret_cast<uint4*>(p) = v;
               } else {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -530,7 +542,7 @@ int fp8_gemm_wide(const Fp8Gemm& g, cudaStream_t stream) {
   a.sy = g.sy; a.ldsy = g.ldsy;
   a.status = g.status;
   const int es = gated ? 1 : g.y_dtype == GPTQ_F32 ? 4 : 2;
-  a.y_vec = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.ldy * es % 16 == 0;
+  a.y_align = row_align(g.y, g.ldy * es);
   a.tiles_m = (g.m + 2 * BM - 1) / (2 * BM);
   const int cols = gated ? BB : 2 * BB;
   a.tiles_n = (g.n + cols - 1) / cols;

@@ -268,13 +268,13 @@ GPTQ_DEV uint32_t pack2(float a, float b, int dtype) {
 
 // Four consecutive columns of an output row from their sums: v[0] as it is in the type of Y (NW = 1),
 // or h = silu(v[0]) v[1] in the format (NW = 2), where the whole warp holds the row's 128 columns
-// of one scale, which goes to sy. vec: Y's rows are 16-byte aligned. row_at: element offset of the
-// row; columns from n on do not exist.
+// of one scale, which goes to sy. align: of Y's rows, in bytes. row_at: element offset of the row;
+// columns from n on do not exist.
 template <int NW>
 GPTQ_DEV void store_row4(const float4 (&v)[NW], void* y, long long row_at, int col, int n,
-                         int y_dtype, bool vec, float* sy) {
+                         int y_dtype, int align, float* sy) {
   float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-  vec = vec && col + 4 <= n;
+  const bool vec = col + 4 <= n && align >= (NW == 2 ? 4 : y_dtype == GPTQ_F32 ? 16 : 8);
   if constexpr (NW == 2) {
     const float u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t mx = 0;

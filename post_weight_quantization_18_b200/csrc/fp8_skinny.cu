@@ -52,7 +52,7 @@ struct SkinnyArgs {
   float* sy;
   long long ldsy;
   int y_dtype;
-  bool y_vec;   // rows of y are 16-byte aligned
+  int y_align;  // of the rows of y, in bytes
   int ksplit;   // CTAs of a cluster
   int32_t* status;
 };
@@ -267,7 +267,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             }
         }
         gptq::store_row4<NW>(v, args.y, (long long)r * args.ldy, block * 128 + lane * 4, args.N,
-                             args.y_dtype, args.y_vec,
+                             args.y_dtype, args.y_align,
                              args.sy + (NW == 2 ? (long long)r * args.ldsy + block : 0));
       }
     }
@@ -315,13 +315,15 @@ int fp8_skinny(const Fp8Gemm& g, cudaStream_t stream) {
   a.sy = g.sy; a.ldsy = g.ldsy;
   a.status = g.status;
   const int es = gated ? 1 : g.y_dtype == GPTQ_F32 ? 4 : 2;
-  a.y_vec = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.ldy * es % 16 == 0;
+  a.y_align = row_align(g.y, g.ldy * es);
   const int blocks = (g.n + BM - 1) / BM;
-  // As many CTAs along K as the SMs hold two of, each with four blocks of K at least.
-  const int sms = num_sms();
-  a.ksplit = 1;
-  while (a.ksplit < 8 && blocks * (a.ksplit + 1) <= 2 * sms && a.nkb >= 4 * (a.ksplit + 1))
-    ++a.ksplit;
+  // As many CTAs along K as clusters of them are resident at once, each with four blocks of K at least.
+  auto resident = [&](int size) {
+    return gated ? resident_clusters(Cfg<2, 16>::THREADS, Cfg<2, 16>::SMEM, size)
+                 : resident_clusters(Cfg<1, 16>::THREADS, Cfg<1, 16>::SMEM, size);
+  };
+  a.ksplit = a.nkb >= 32 ? 8 : a.nkb >= 8 ? a.nkb / 4 : 1;
+  while (a.ksplit > 1 && blocks > resident(a.ksplit)) --a.ksplit;
   if (gated)
     return g.m <= 16 ? launch<2, 16>(g, a, blocks, stream) : launch<2, 32>(g, a, blocks, stream);
   return g.m <= 16 ? launch<1, 16>(g, a, blocks, stream) : launch<1, 32>(g, a, blocks, stream);

@@ -48,7 +48,7 @@ struct ThinArgs {
   float* sy;
   long long ldsy;
   int y_dtype;
-  bool y_vec;         // rows of y are 16-byte aligned
+  int y_align;        // of the rows of y, in bytes
   int x_rows;         // rows of the X box
   int tiles_n, n_tiles;
   int ksplit;         // CTAs of a cluster along K
@@ -411,7 +411,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
               const uint64_t a = acc[0][c][2 * e], b = acc[0][c][2 * e + 1];
               o[e] = gptq::e4m3x4(lo2(a) * inv, hi2(a) * inv, lo2(b) * inv, hi2(b) * inv);
             }
-            if (args.y_vec && col0 + 16 * c + 16 <= args.N) {
+            if (args.y_align == 16 && col0 + 16 * c + 16 <= args.N) {
               *reinterpret_cast<uint4*>(q + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
             } else {
 #pragma unroll
@@ -425,7 +425,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
         const long long at = (long long)row * args.ldy + col0;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          const bool vec = args.y_vec && col0 + 16 * c + 16 <= args.N;
+          const bool vec = col0 + 16 * c + 16 <= args.N;  // rows are 16-byte aligned here
           if (vec && args.y_dtype == GPTQ_F32) {
             float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.y) + at + 16 * c);
 #pragma unroll
@@ -490,7 +490,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
           if (live) {
             const long long row = row_tile(t0) * BM + r;
             gptq::store_row4<NW>(v, args.y, row * args.ldy, tile_col + c4, args.N, args.y_dtype,
-                                 args.y_vec,
+                                 args.y_align,
                                  args.sy + (NW == 2 ? row * args.ldsy + tile_col / 128 : 0));
           }
         }
@@ -589,11 +589,20 @@ static int plain_tile(const Fp8Gemm& g, int sms) {
   return best;
 }
 
+// Clusters of `size` CTAs, one CTA an SM, that the device holds at once.
+static int resident(int size) {
+  return resident_clusters(THREADS, SMEM_BYTES, size);
+}
+
 long long fp8_thin_cost(const Fp8Gemm& g) {
   const int sms = num_sms();
   if (g.w[1] == nullptr) return tile_cost(g, plain_tile(g, sms), sms);
-  const long long tiles = (long long)((g.m + BM - 1) / BM) * ((g.n + 127) / 128);
-  return (tiles + sms - 1) / sms * 400;  // 256 rows, of two weights
+  // Gated pair: 32 or 64 rows of each weight where clusters hold all groups (64 x 4096 x 4096: 0.33 us),
+  // else 128 (64 x 11008 x 4096: 0.6 us).
+  const long long groups = (long long)((g.m + BM - 1) / BM) * ((g.n + 127) / 128);
+  if (groups <= resident(4)) return 195;
+  if (groups <= resident(2)) return 300;
+  return (groups + sms - 1) / sms * 355;
 }
 
 int fp8_thin(const Fp8Gemm& g, cudaStream_t stream) {
@@ -612,28 +621,37 @@ int fp8_thin(const Fp8Gemm& g, cudaStream_t stream) {
   a.sy = g.sy; a.ldsy = g.ldsy;
   a.status = g.status;
   const int es = gated ? 1 : g.y_dtype == GPTQ_F32 ? 4 : 2;
-  a.y_vec = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && g.ldy * es % 16 == 0;
+  a.y_align = row_align(g.y, g.ldy * es);
   // Rows of X that a tile can hold: a call of few rows brings only those (whole groups of the
   // swizzle's eight rows); what the MMA reads behind them feeds accumulator rows nobody reads.
   a.x_rows = g.m >= BM ? BM : (g.m + 7) / 8 * 8;
   a.ksplit = 1;
   const long long tiles_m = (g.m + BM - 1) / BM;
   auto tiles = [&](int cols) { return tiles_m * ((g.n + cols - 1) / cols); };
+  // Clusters are used where they are all resident at once: of one CTA an SM, that is fewer than the
+  // SMs divided by their size (15 of eight, not 18).
   if (gated) {
-    if (tiles(128) * 2 > sms) return launch<2, 4, false>(g, a, sms, stream);
-    if (tiles(128) * 4 > sms) return launch<2, 2, true>(g, a, sms, stream);
-    if (tiles(128) * 8 <= sms && a.nkb >= 16) a.ksplit = 2;  // two stages of four blocks each
-    return launch<2, 1, true>(g, a, sms, stream);
+    const long long groups = tiles(128);
+    if (groups <= resident(4)) {
+      if (groups <= resident(8) && a.nkb >= 16) a.ksplit = 2;  // two stages of four blocks each
+      return launch<2, 1, true>(g, a, sms, stream);
+    }
+    if (groups <= resident(2)) return launch<2, 2, true>(g, a, sms, stream);
+    return launch<2, 4, false>(g, a, sms, stream);
   }
-  if (tiles(32) * 2 <= sms && a.nkb >= 16) {
-    while (a.ksplit < 8 && tiles(32) * a.ksplit * 2 <= sms && a.nkb >= 16 * a.ksplit) a.ksplit *= 2;
-    return launch<1, 1, true>(g, a, sms, stream);
-  }
+  for (int s = 8; s >= 2; --s)
+    if (a.nkb >= 8 * s && tiles(32) <= resident(s)) {
+      a.ksplit = s;
+      return launch<1, 1, true>(g, a, sms, stream);
+    }
+  // Rows that 16-byte stores cannot address go out through shared memory, a warp along each row: the
+  // direct stores, one row a lane, took 10 of 19 us at 2000 x 300 x 4096.
+  const bool direct = a.y_align == 16;
   switch (plain_tile(g, sms)) {
-    case 1: return launch<1, 1, false>(g, a, sms, stream);
-    case 2: return launch<1, 2, false>(g, a, sms, stream);
-    case 3: return launch<1, 3, false>(g, a, sms, stream);
-    default: return launch<1, 4, false>(g, a, sms, stream);
+    case 1: return direct ? launch<1, 1, false>(g, a, sms, stream) : launch<1, 1, true>(g, a, sms, stream);
+    case 2: return direct ? launch<1, 2, false>(g, a, sms, stream) : launch<1, 2, true>(g, a, sms, stream);
+    case 3: return direct ? launch<1, 3, false>(g, a, sms, stream) : launch<1, 3, true>(g, a, sms, stream);
+    default: return direct ? launch<1, 4, false>(g, a, sms, stream) : launch<1, 4, true>(g, a, sms, stream);
   }
 }
 
