@@ -101,6 +101,28 @@ def test_gated_matches_oracle_where_the_sigmoid_bends(m, n, k):
     run_gated(m, n, k, seed=m + n + k, scale=0.05 / (64.0 * k ** 0.25))
 
 
+# Shapes that take each variant of the kernels on a B200: clusters of different size along K, tiles of
+# 32, 64, 96 (which span two weight blocks) and 128 weight rows, several rounds of CTAs, output rows that
+# 16-byte stores cannot address, pairs of CTAs with odd numbers of row tiles.
+VARIANTS = [
+    (8, 4224, 4096), (32, 11008, 512), (31, 129, 8200), (16, 20000, 384),
+    (40, 512, 4096), (40, 480, 5200), (33, 8192, 256), (100, 11008, 256), (40, 14000, 200),
+    (150, 8192, 256), (150, 8191, 264), (40, 11003, 256), (34, 2999, 1024), (130, 4097, 300),
+    (1030, 2051, 264), (700, 9000, 136), (2100, 1100, 512),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m,n,k", VARIANTS)
+def test_gemm_variants(m, n, k, dtype):
+    run_gemm(m, n, k, dtype, seed=m + n + k)
+
+
+@pytest.mark.parametrize("m,n,k", VARIANTS + [(40, 6144, 256), (129, 3000, 1536)])
+def test_gated_variants(m, n, k):
+    run_gated(m, n, k, seed=m + n + k, scale=0.05 / (64.0 * k ** 0.25))
+
+
 @pytest.mark.parametrize("m", [3, 40, 140])
 @pytest.mark.parametrize("kw", [dict(ld=300), dict(ld=301), dict(ld=304, offset=1),
                                 dict(ld=320, offset=8), dict(ld=384, offset=16)])
@@ -161,7 +183,8 @@ def test_nan_stays_in_its_row_or_column(m):
     assert torch.equal(Y[~want], Y0[~want])
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 512, 4096), (40, 512, 4096), (300, 640, 1024)])
+@pytest.mark.parametrize("m,n,k", [(1, 512, 4096), (40, 512, 4096), (300, 640, 1024),
+                                   (1030, 2050, 384)])
 def test_status_repeats_and_capture(m, n, k):
     """Skipped while the status holds an error; two calls give the same bits, and so does a replay
     of a captured pair, beside a direct call on another stream."""
