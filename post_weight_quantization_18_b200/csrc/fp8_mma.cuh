@@ -308,4 +308,51 @@ GPTQ_DEV void store_row4(const float4 (&v)[NW], void* y, long long row_at, int c
   }
 }
 
+// The rows of an output tile, added up over the CTAs of a cluster that shared K, always in their order:
+// rows first, first + stride, ... below `end`, four columns a lane. at(w, r) is the shared-memory
+// address of row r's sums of weight w, who(s) the CTA with part s of K; done(r, v) takes the row (it is
+// called by all lanes). Eight loads are in flight, of one row or of several.
+template <int NW, int R, typename At, typename Who, typename Done>
+GPTQ_DEV void add_up_rows(int first, int stride, int end, int ksplit, At at, Who who, Done done) {
+  constexpr int S = 8 / R;
+  for (int r0 = first; r0 < end; r0 += R * stride) {
+    float4 p[R][S][NW];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s < ksplit) {
+#pragma unroll
+          for (int w = 0; w < NW; ++w) p[i][s][w] = ld_cluster(at(w, min(r0 + i * stride, end - 1)), who(s));
+        }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (r0 + i * stride >= end) break;
+      float4 v[NW];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        v[w] = p[i][0][w];
+#pragma unroll
+        for (int s = 1; s < S; ++s)
+          if (s < ksplit) {
+            v[w].x += p[i][s][w].x;
+            v[w].y += p[i][s][w].y;
+            v[w].z += p[i][s][w].z;
+            v[w].w += p[i][s][w].w;
+          }
+      }
+      done(r0 + i * stride, v);
+    }
+  }
+}
+template <int NW, typename At, typename Who, typename Done>
+GPTQ_DEV void add_up(int first, int stride, int end, int ksplit, At at, Who who, Done done) {
+  if (ksplit <= 2)
+    add_up_rows<NW, 4>(first, stride, end, ksplit, at, who, done);
+  else if (ksplit <= 4)
+    add_up_rows<NW, 2>(first, stride, end, ksplit, at, who, done);
+  else
+    add_up_rows<NW, 1>(first, stride, end, ksplit, at, who, done);
+}
+
 }  // namespace gptq

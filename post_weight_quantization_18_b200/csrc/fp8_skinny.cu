@@ -1,5 +1,5 @@
-// fp8_skinny.cu — the products of the e4m3 format for up to 32 rows of activations (decoding), where
-// the time is that of streaming the weight.
+// fp8_skinny.cu — the products of the e4m3 format for few rows of activations (decoding), where the time
+// is that of streaming the weight: up to 32 rows, in the gated pair up to 64.
 //
 // The operands change places: the 128 rows of a weight block are the M of the MMAs (lanes of tensor
 // memory), the activation rows their N. A thread of the epilogue then owns one weight row and reads
@@ -14,7 +14,7 @@
 // also has the whole 128 columns of the row's scale.
 // Two CTAs share an SM, so that one's start and end pass behind the other's stream.
 // Measured (B200): 1 x 8192 x 28672 in 37.3 us (6.3 TB/s, 0.98 of the measured copy rate), 8 x 11008 x
-// 4096 gated in 18.4 us (4.9 TB/s), 16 x 11008 x 4096 in 11.0 us (a loop that only streams this
+// 4096 gated in 18.4 us (4.9 TB/s), 64 x 11008 x 4096 gated in 22.0 us, 16 x 11008 x 4096 in 11.0 us (a loop that only streams this
 // weight: 10.3), 1 x 4096 x 4096 in 5.8 us with the weight in L2, of which about 4 are the
 // kernel's start, the latency of its first load and the cluster's exchange.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-7 epilogue (gated pair: 8-11 the
@@ -25,23 +25,26 @@ namespace {
 
 using gptq::bar_wait;
 using gptq::bar_wait_rest;
-using Scales = gptq::ScaleRing<32>;
 
 constexpr int BM = 128, BK = 128;
 constexpr int W_TILE = BM * BK;  // 16 KB
-constexpr int NBUF = 4;          // accumulators
 constexpr int PITCH = BM + 4;    // floats of a row of sums
 constexpr int EPI_WARP0 = 4;
 
 template <int NW, int MT>
 struct Cfg {
+  using Scales = gptq::ScaleRing<(MT > 32 ? MT : 32)>;
   static constexpr int THREADS = 128 + 128 * NW;
+  // Two, but for the gated pair of 64 rows, whose 64 sums a thread of 384 take the registers of one.
+  static constexpr int CTAS_PER_SM = NW * MT > 64 ? 1 : 2;
+  static constexpr int NBUF = 4;  // accumulators
   static constexpr int STAGE_BYTES = NW * W_TILE + MT * BK;
-  static constexpr int STAGES = 104 * 1024 / STAGE_BYTES;  // two CTAs per SM
+  static constexpr int STAGES = (CTAS_PER_SM == 2 ? 102 : 204) * 1024 / STAGE_BYTES;
   static constexpr int RING = STAGES * STAGE_BYTES;
   static constexpr int SMEM = RING + Scales::BYTES + 512 + 1024;
-  static constexpr uint32_t TMEM_COLS = NBUF * NW * MT;  // 64, 128 or 256
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024 && STAGES >= 2, "two CTAs per SM");
+  static constexpr uint32_t TMEM_COLS = NBUF * NW * MT;  // 64 to 512
+  static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024 && STAGES >= 2, "shared memory");
+  static_assert(CTAS_PER_SM * TMEM_COLS <= 512, "tensor memory");
   static_assert(NW * MT * PITCH * 4 <= RING, "sums");
 };
 
@@ -62,10 +65,12 @@ struct SkinnyArgs {
 };
 
 template <int NW, int MT>
-__global__ void __launch_bounds__(Cfg<NW, MT>::THREADS, 2)
+__global__ void __launch_bounds__(Cfg<NW, MT>::THREADS, Cfg<NW, MT>::CTAS_PER_SM)
 fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
                   const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ SkinnyArgs args) {
   using C = Cfg<NW, MT>;
+  using Scales = typename C::Scales;
+  constexpr int NBUF = C::NBUF;
   constexpr uint32_t IDESC = gptq::instr_desc(/*e4m3*/ 0, 0, 0, BM, MT);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (gptq::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -210,25 +215,34 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       gptq::tc_fence_after();
       const float2 sw2 = scales.blocks(chunk, j);
       const uint64_t sw = gptq::pair2(NW == 2 && w ? sw2.y : sw2.x);
-      uint32_t r[MT / 16][16];
-#pragma unroll
-      for (int c = 0; c < MT / 16; ++c)
-        gptq::tmem_ld_32x32b_x16(acc_col + (uint32_t)(buf * NW * MT + 16 * c), r[c]);
-      gptq::tmem_ld_wait();
-      gptq::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) gptq::bar_arrive(acc_empty(buf));
+      // Sixteen columns (activation rows) a load, two loads at a time.
+      const uint32_t col = acc_col + (uint32_t)(buf * NW * MT), freed = acc_empty(buf);
       if (++buf == NBUF) { buf = 0; acc_phase ^= 1; }
-      acc_ready = gptq::bar_poll(acc_full(buf), acc_phase);
 #pragma unroll
-      for (int c = 0; c < MT / 16; ++c) {
-        gptq::settled(r[c]);
+      for (int c0 = 0; c0 < MT / 16; c0 += 2) {
+        uint32_t r[2][16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 sx = scales.rows4(chunk, j, 16 * c + 4 * e);
-          uint64_t* a = acc + 8 * c + 2 * e;
-          gptq::fma2(a[0], r[c][4 * e], r[c][4 * e + 1], gptq::mul2(sx.x, sx.y, sw));
-          gptq::fma2(a[1], r[c][4 * e + 2], r[c][4 * e + 3], gptq::mul2(sx.z, sx.w, sw));
+        for (int i = 0; i < 2; ++i)
+          if (c0 + i < MT / 16) gptq::tmem_ld_32x32b_x16(col + (uint32_t)(16 * (c0 + i)), r[i]);
+        gptq::tmem_ld_wait();
+        if (c0 + 2 >= MT / 16) {  // all of it is in registers: the accumulator is free
+          gptq::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) gptq::bar_arrive(freed);
+          acc_ready = gptq::bar_poll(acc_full(buf), acc_phase);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = c0 + i;
+          if (c >= MT / 16) break;
+          gptq::settled(r[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 sx = scales.rows4(chunk, j, 16 * c + 4 * e);
+            uint64_t* a = acc + 8 * c + 2 * e;
+            gptq::fma2(a[0], r[i][4 * e], r[i][4 * e + 1], gptq::mul2(sx.x, sx.y, sw));
+            gptq::fma2(a[1], r[i][4 * e + 2], r[i][4 * e + 3], gptq::mul2(sx.z, sx.w, sw));
+          }
         }
       }
       if (j == Scales::KC - 1) {
@@ -251,29 +265,15 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     gptq::cluster_sync();
     if (!skip) {
       // Rows are dealt out to the warps of all CTAs in turn.
-      for (int r = (int)rank * 4 * NW + warp - EPI_WARP0; r < args.M; r += args.ksplit * 4 * NW) {
-        float4 v[NW];
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          const uint32_t at = smem + (uint32_t)((i * MT + r) * PITCH + lane * 4) * 4;
-          float4 p[8];
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            if (s < args.ksplit) p[s] = gptq::ld_cluster(at, s);
-          v[i] = p[0];
-#pragma unroll
-          for (int s = 1; s < 8; ++s)
-            if (s < args.ksplit) {
-              v[i].x += p[s].x;
-              v[i].y += p[s].y;
-              v[i].z += p[s].z;
-              v[i].w += p[s].w;
-            }
-        }
-        gptq::store_row4<NW>(v, args.y, (long long)r * args.ldy, block * 128 + lane * 4, args.N,
-                             args.y_dtype, args.y_align,
-                             args.sy + (NW == 2 ? (long long)r * args.ldsy + block : 0));
-      }
+      gptq::add_up<NW>(
+          (int)rank * 4 * NW + warp - EPI_WARP0, args.ksplit * 4 * NW, args.M, args.ksplit,
+          [&](int i, int r) { return smem + (uint32_t)((i * MT + r) * PITCH + lane * 4) * 4; },
+          [](int s) { return (uint32_t)s; },
+          [&](int r, const float4(&v)[NW]) {
+            gptq::store_row4<NW>(v, args.y, (long long)r * args.ldy, block * 128 + lane * 4, args.N,
+                                 args.y_dtype, args.y_align,
+                                 args.sy + (NW == 2 ? (long long)r * args.ldsy + block : 0));
+          });
     }
     gptq::cluster_sync();  // no CTA leaves while its sums may still be read
   }
@@ -322,15 +322,15 @@ int fp8_skinny(const Fp8Gemm& g, cudaStream_t stream) {
   a.y_align = row_align(g.y, g.ldy * es);
   const int blocks = (g.n + BM - 1) / BM;
   // As many CTAs along K as clusters of them are resident at once, each with four blocks of K at least.
-  auto resident = [&](int size) {
-    return gated ? resident_clusters(Cfg<2, 16>::THREADS, Cfg<2, 16>::SMEM, size)
-                 : resident_clusters(Cfg<1, 16>::THREADS, Cfg<1, 16>::SMEM, size);
+  auto run = [&](auto launch, int threads, int smem) {
+    a.ksplit = a.nkb >= 32 ? 8 : a.nkb >= 8 ? a.nkb / 4 : 1;
+    while (a.ksplit > 1 && blocks > resident_clusters(threads, smem, a.ksplit)) --a.ksplit;
+    return launch(g, a, blocks, stream);
   };
-  a.ksplit = a.nkb >= 32 ? 8 : a.nkb >= 8 ? a.nkb / 4 : 1;
-  while (a.ksplit > 1 && blocks > resident(a.ksplit)) --a.ksplit;
-  if (gated)
-    return g.m <= 16 ? launch<2, 16>(g, a, blocks, stream) : launch<2, 32>(g, a, blocks, stream);
-  return g.m <= 16 ? launch<1, 16>(g, a, blocks, stream) : launch<1, 32>(g, a, blocks, stream);
+#define FP8_SKINNY(NW, MT) run(launch<NW, MT>, Cfg<NW, MT>::THREADS, Cfg<NW, MT>::SMEM)
+  if (gated) return g.m <= 16 ? FP8_SKINNY(2, 16) : g.m <= 32 ? FP8_SKINNY(2, 32) : FP8_SKINNY(2, 64);
+  return g.m <= 16 ? FP8_SKINNY(1, 16) : FP8_SKINNY(1, 32);
+#undef FP8_SKINNY
 }
 
 }  // namespace gptq_host

@@ -15,7 +15,7 @@
 //                      pair's scale and then K. Every CTA leaves its sums in shared memory, the
 //                      rows are added up over the cluster, always in the same order.
 // Measured (B200): 64 x 8192 x 28672 in 45 us (5.3 TB/s), 64 x 11008 x 4096 in 12.0 us (a loop that
-// only streams this weight: 10.3), 512 x 4096 x 4096 in 12.8 us, gated 64 x 11008 x 4096 in 23.4 us.
+// only streams this weight: 10.3), 512 x 4096 x 4096 in 12.8 us, gated 100 x 11008 x 4096 in 24.1 us.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-11 epilogue (two per quarter of the TMEM
 // lanes, half the tile's columns each). Every wait is bounded as in fp8_gemm.cu.
 #include <cudaTypedefs.h>
@@ -465,37 +465,20 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
         const int sub = lane / LPR, c4 = (lane % LPR) * 4;
         const int part = c4 / BN;  // the CTA along the columns that holds them
         const int tile_col = (t0 % args.tiles_n) * (CN * BN);
-        // Rows are dealt out to the warps of all CTAs in turn.
-        for (int r0 = ((int)rank * N_EPI + warp - EPI_WARP0) * RPW; r0 < rows;
-             r0 += csize * N_EPI * RPW) {
-          const int r = r0 + sub;
-          const bool live = sub < RPW && r < rows;
-          float4 v[NW];
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const uint32_t at =
-                smem + (uint32_t)((w * BM + min(r, BM - 1)) * PITCH + c4 % BN) * 4;
-            float4 p[8];
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-              if (s < args.ksplit) p[s] = gptq::ld_cluster(at, s * CN + part);
-            v[w] = p[0];
-#pragma unroll
-            for (int s = 1; s < 8; ++s)
-              if (s < args.ksplit) {
-                v[w].x += p[s].x;
-                v[w].y += p[s].y;
-                v[w].z += p[s].z;
-                v[w].w += p[s].w;
-              }
-          }
-          if (live) {
-            const long long row = row_tile(t0) * BM + r;
-            gptq::store_row4<NW>(v, args.y, row * args.ldy, tile_col + c4, args.N, args.y_dtype,
-                                 args.y_align,
-                                 args.sy + (NW == 2 ? row * args.ldsy + tile_col / 128 : 0));
-          }
-        }
+        // Rows are dealt out to the warps of all CTAs in turn, RPW at a time.
+        gptq::add_up<NW>(
+            (int)rank * N_EPI + warp - EPI_WARP0, csize * N_EPI, (rows + RPW - 1) / RPW, args.ksplit,
+            [&](int w, int r) {
+              return smem + (uint32_t)((w * BM + min(r * RPW + sub, BM - 1)) * PITCH + c4 % BN) * 4;
+            },
+            [&](int s) { return (uint32_t)(s * CN + part); },
+            [&](int r, const float4(&v)[NW]) {
+              const long long row = row_tile(t0) * BM + r * RPW + sub;
+              if (sub < RPW && r * RPW + sub < rows)
+                gptq::store_row4<NW>(v, args.y, row * args.ldy, tile_col + c4, args.N, args.y_dtype,
+                                     args.y_align,
+                                     args.sy + (NW == 2 ? row * args.ldsy + tile_col / 128 : 0));
+            });
       }
       gptq::cluster_sync();  // no CTA leaves while its sums may still be read
     }
@@ -599,8 +582,8 @@ static int resident(int size) {
 long long fp8_thin_cost(const Fp8Gemm& g) {
   const int sms = num_sms();
   if (g.w[1] == nullptr) return tile_cost(g, plain_tile(g, sms), sms);
-  // Gated pair: 32 or 64 rows of each weight where clusters hold all groups (64 x 4096 x 4096: 0.33 us),
-  // else 128 (64 x 11008 x 4096: 0.6 us).
+  // Gated pair: 32 or 64 rows of each weight where clusters hold all groups (100 x 4096 x 4096: 15.1 us, a
+  // block 0.33), else 128 (100 x 11008 x 4096: 24.1 us, a block 0.6).
   const long long groups = (long long)((g.m + BM - 1) / BM) * ((g.n + 127) / 128);
   if (groups <= resident(4)) return 195;
   if (groups <= resident(2)) return 300;

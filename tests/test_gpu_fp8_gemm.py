@@ -118,7 +118,15 @@ def test_gemm_variants(m, n, k, dtype):
     run_gemm(m, n, k, dtype, seed=m + n + k)
 
 
-@pytest.mark.parametrize("m,n,k", VARIANTS + [(40, 6144, 256), (129, 3000, 1536)])
+# The gated pair's own: its largest tile with the weight as the MMAs' M, and the smallest without.
+GATED_VARIANTS = [
+    (40, 6144, 256), (129, 3000, 1536), (64, 4224, 4096), (64, 20000, 384), (50, 129, 8200),
+    (33, 1, 1), (65, 512, 4096), (72, 1000, 1100), (66, 2304, 2048), (80, 6144, 256),
+    (90, 13999, 256),
+]
+
+
+@pytest.mark.parametrize("m,n,k", VARIANTS + GATED_VARIANTS)
 def test_gated_variants(m, n, k):
     run_gated(m, n, k, seed=m + n + k, scale=0.05 / (64.0 * k ** 0.25))
 
