@@ -277,6 +277,7 @@ int fp8_gemm_wide(const Fp8Gemm& a, cudaStream_t stream);
 long long fp8_wide_cost(const Fp8Gemm& a);
 int fp8_thin(const Fp8Gemm& a, cudaStream_t stream);
 long long fp8_thin_cost(const Fp8Gemm& a);
+bool fp8_skinny_takes(const Fp8Gemm& a);  // where it is the fastest
 int fp8_skinny(const Fp8Gemm& a, cudaStream_t stream);  // up to 32 rows, gated 64
 // A tensor map of whole blocks of 128 columns: boxes of 128 bytes x box_rows x box_blocks.
 int make_tmap_blocks(CUtensorMap* map, const uint8_t* base, uint64_t rows, uint64_t ld,

@@ -22,13 +22,9 @@ inline bool operand_ok(const uint8_t* q, const float* s) {
   return q != nullptr && s != nullptr && aligned(s, 4);
 }
 
-// Few rows go to the kernel that has the weight as the MMAs' M. Measured on both sides (us, that kernel /
-// fp8_thin): plain 32 x 11008 x 4096 12.0 / 12.3, 64 x 11008 x 4096 13.3 / 12.0, 64 x 4096 x 4096
-// 10.1 / 7.8, 64 x 8192 x 8192 16.6 / 15.3; gated 64 x 11008 x 4096 22.0 / 23.4, 64 x 4096 x 4096
-// 12.7 / 14.7, 64 x 2048 x 2048 9.0 / 9.6.
 int gemm_launch(const gptq_host::Fp8Gemm& a, cudaStream_t stream) {
   const int rc = !gptq_host::fp8_tma_takes(a) ? gptq_host::fp8_gemm_simt(a, stream)
-                 : a.m <= (a.w[1] ? 64 : 32)       ? gptq_host::fp8_skinny(a, stream)
+                 : gptq_host::fp8_skinny_takes(a)  ? gptq_host::fp8_skinny(a, stream)
                  : gptq_host::fp8_wide_cost(a) < gptq_host::fp8_thin_cost(a)
                      ? gptq_host::fp8_gemm_wide(a, stream)
                      : gptq_host::fp8_thin(a, stream);

@@ -173,17 +173,20 @@ __device__ __forceinline__ void flush_rows(const TcArgs& a, uint32_t st, int row
       }
     }
   } else {  // a row at a time, one word a lane, so that the warp's stores are neighbours all the same
-    const int col = col0 + lane * (4 / ES);
-    for (int r = 0; r < 32 && row0 + r < a.M; ++r) {
-      const uint32_t w = gptq::flag_read(staged(st, r, lane >> 2) + (lane & 3) * 4);
-      uint8_t* p = reinterpret_cast<uint8_t*>(a.y) + ((long long)(row0 + r) * a.ldy + col) * ES;
-      if (ES == 4 || (a.y_align >= 4 && col + 1 < a.N)) {
-        if (col < a.N) *reinterpret_cast<uint32_t*>(p) = w;
-      } else {
+    uint8_t* p = reinterpret_cast<uint8_t*>(a.y) + ((long long)row0 * a.ldy + col0) * ES;
+    const long long pitch = a.ldy * ES;
+    const int rows = a.M - row0;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 4) {
+      uint32_t w[4], next[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (col + e < a.N) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w >> (e * 16));
-      }
+      for (int i = 0; i < 4; ++i)
+        w[i] = gptq::flag_read(staged(st, r0 + i, lane >> 2) + (lane & 3) * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) next[i] = ES == 4 ? 0u : __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i, p += pitch)
+        gptq::store_word<ES, 32>(p, lane, w[i], next[i], r0 + i < rows ? a.N - col0 : 0);
     }
   }
   __syncwarp();

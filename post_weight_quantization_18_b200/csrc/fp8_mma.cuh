@@ -229,6 +229,12 @@ GPTQ_DEV uint64_t mul2(float a, float b, uint64_t f2) {  // (a, b) * f
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v), "l"(f2));
   return r;
 }
+GPTQ_DEV uint64_t add2(uint64_t v, float a, float b) {  // v + (a, b)
+  uint64_t p, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(v), "l"(p));
+  return r;
+}
 GPTQ_DEV float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
 GPTQ_DEV float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
@@ -241,10 +247,23 @@ GPTQ_DEV void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-GPTQ_DEV void cluster_sync() {
+GPTQ_DEV void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+GPTQ_DEV void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+GPTQ_DEV void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// The maximum with a word in the shared memory of a CTA of the cluster.
+GPTQ_DEV void max_cluster(uint32_t saddr, uint32_t rank, uint32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 GPTQ_DEV float4 ld_cluster(uint32_t saddr, uint32_t rank) {
   uint32_t a;
@@ -308,13 +327,44 @@ GPTQ_DEV void store_row4(const float4 (&v)[NW], void* y, long long row_at, int c
   }
 }
 
+GPTQ_DEV void store_if(bool on, void* p, uint32_t v) {  // a branch would cost more than the store
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q st.global.u32 [%0], %1;\n\t}" ::"l"(p),
+               "r"(v), "r"((uint32_t)on)
+               : "memory");
+}
+GPTQ_DEV void store_if(bool on, void* p, uint16_t v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q st.global.u16 [%0], %1;\n\t}" ::"l"(p),
+               "h"(v), "r"((uint32_t)on)
+               : "memory");
+}
+// One 4-byte word a lane of WORDS neighbours, which begin a row's piece at p, `left` elements of ES bytes
+// before the row's end: this lane's word i and its neighbour's. Where 2-byte elements start between
+// words, every lane takes one element from its neighbour, so that whole words are stored all the
+// same, and the first and the last lane store one element each (8000 x 8191 x 512 with two 2-byte
+// stores a lane: 108 us, with branches around these: 125, so: 92).
+template <int ES, int WORDS>
+GPTQ_DEV void store_word(uint8_t* p, int i, uint32_t w, uint32_t next, int left) {
+  if constexpr (ES == 4) {
+    store_if(i < left, p + 4 * i, w);
+  } else {
+    const int odd = (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+    const int at = 2 * i + odd, end = min(2 * WORDS, left);
+    const uint32_t v = __funnelshift_r(w, next, odd * 16);
+    uint8_t* q = p + 2 * at;
+    store_if(at + 1 < end, q, v);
+    const bool first = odd && i == 0;
+    store_if(first ? end > 0 : at + 1 == end, first ? p : q, (uint16_t)(first ? w : v));
+    if (end == 2 && first) store_if(true, q, (uint16_t)v);  // both ends are this lane's
+  }
+}
+
 // The rows of an output tile, added up over the CTAs of a cluster that shared K, always in their order:
 // rows first, first + stride, ... below `end`, four columns a lane. at(w, r) is the shared-memory
 // address of row r's sums of weight w, who(s) the CTA with part s of K; done(r, v) takes the row (it is
-// called by all lanes). Eight loads are in flight, of one row or of several.
-template <int NW, int R, typename At, typename Who, typename Done>
+// called by all lanes). Eight loads are in flight, of one row or of several. Where K was not shared
+// the row is read as the CTA's own memory: by way of the cluster that takes 900 cycles.
+template <int NW, int R, int S, typename At, typename Who, typename Done>
 GPTQ_DEV void add_up_rows(int first, int stride, int end, int ksplit, At at, Who who, Done done) {
-  constexpr int S = 8 / R;
   for (int r0 = first; r0 < end; r0 += R * stride) {
     float4 p[R][S][NW];
 #pragma unroll
@@ -323,7 +373,10 @@ GPTQ_DEV void add_up_rows(int first, int stride, int end, int ksplit, At at, Who
       for (int s = 0; s < S; ++s)
         if (s < ksplit) {
 #pragma unroll
-          for (int w = 0; w < NW; ++w) p[i][s][w] = ld_cluster(at(w, min(r0 + i * stride, end - 1)), who(s));
+          for (int w = 0; w < NW; ++w) {
+            const uint32_t a = at(w, min(r0 + i * stride, end - 1));
+            p[i][s][w] = S == 1 ? lds_f32x4(a) : ld_cluster(a, who(s));
+          }
         }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -347,12 +400,14 @@ GPTQ_DEV void add_up_rows(int first, int stride, int end, int ksplit, At at, Who
 }
 template <int NW, typename At, typename Who, typename Done>
 GPTQ_DEV void add_up(int first, int stride, int end, int ksplit, At at, Who who, Done done) {
-  if (ksplit <= 2)
-    add_up_rows<NW, 4>(first, stride, end, ksplit, at, who, done);
+  if (ksplit == 1)
+    add_up_rows<NW, 4, 1>(first, stride, end, ksplit, at, who, done);
+  else if (ksplit == 2)
+    add_up_rows<NW, 4, 2>(first, stride, end, ksplit, at, who, done);
   else if (ksplit <= 4)
-    add_up_rows<NW, 2>(first, stride, end, ksplit, at, who, done);
+    add_up_rows<NW, 2, 4>(first, stride, end, ksplit, at, who, done);
   else
-    add_up_rows<NW, 1>(first, stride, end, ksplit, at, who, done);
+    add_up_rows<NW, 1, 8>(first, stride, end, ksplit, at, who, done);
 }
 
 }  // namespace gptq

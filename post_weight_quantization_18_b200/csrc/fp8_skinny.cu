@@ -60,7 +60,8 @@ struct SkinnyArgs {
   long long ldsy;
   int y_dtype;
   int y_align;  // of the rows of y, in bytes
-  int ksplit;   // CTAs of a cluster
+  int ksplit;   // CTAs of a cluster, which have kq blocks of K each, the first kr one more
+  int kq, kr;
   int32_t* status;
 };
 
@@ -86,8 +87,9 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   const uint32_t tmem_slot = scales.bars + Scales::BAR_BYTES;
   const uint32_t abort_flag = tmem_slot + 4, skip_flag = tmem_slot + 8;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  uint32_t rank;
+  uint32_t rank, cluster_id;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %clusterid.x;" : "=r"(cluster_id));
 
   gptq::let_next_kernel_start();
   if (threadIdx.x == 0) {
@@ -121,9 +123,10 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   gptq::tc_fence_after();
   const uint32_t tmem_base = gptq::flag_read(tmem_slot);
   const bool skip = gptq::flag_read(skip_flag) != 0;
-  const int block = blockIdx.x / args.ksplit;  // of 128 weight rows
-  const int kb0 = (int)((long long)args.nkb * rank / args.ksplit);
-  const int kb1 = (int)((long long)args.nkb * (rank + 1) / args.ksplit);
+  // The cluster's block of 128 weight rows (no division: it would stand between the CTA and its first load).
+  const int block = (int)cluster_id;
+  const int kb0 = (int)rank * args.kq + min((int)rank, args.kr);
+  const int kb1 = kb0 + args.kq + ((int)rank < args.kr ? 1 : 0);
 
   if (warp < EPI_WARP0) {
     if (skip) {
@@ -305,6 +308,16 @@ int launch(const gptq_host::Fp8Gemm& g, const SkinnyArgs& a, int blocks, cudaStr
 
 namespace gptq_host {
 
+// Measured on both sides (us, this kernel / fp8_thin): plain 32 x 11008 x 4096 12.0 / 12.3, 64 x 11008 x
+// 4096 13.3 / 12.0, 64 x 4096 x 4096 10.1 / 7.8; gated 64 x 11008 x 4096 21.4 / 23.4, 64 x 4096 x 4096
+// 12.0 / 13.2, 34 x 8576 x 1024 8.7 / 10.5, 64 x 256 x 4096 7.1 / 8.4, but 64 x 1024 x 1024 6.8 / 5.7,
+// where K is short and fp8_thin's clusters are all resident.
+bool fp8_skinny_takes(const Fp8Gemm& g) {
+  if (g.m <= 32 || g.w[1] == nullptr) return g.m <= 32;
+  const long long groups = (g.n + BM - 1) / BM;
+  return g.m <= 64 && (g.k > 8 * BK || 4 * groups > num_sms());
+}
+
 int fp8_skinny(const Fp8Gemm& g, cudaStream_t stream) {
   const bool gated = g.w[1] != nullptr;
   SkinnyArgs a{};
@@ -325,6 +338,8 @@ int fp8_skinny(const Fp8Gemm& g, cudaStream_t stream) {
   auto run = [&](auto launch, int threads, int smem) {
     a.ksplit = a.nkb >= 32 ? 8 : a.nkb >= 8 ? a.nkb / 4 : 1;
     while (a.ksplit > 1 && blocks > resident_clusters(threads, smem, a.ksplit)) --a.ksplit;
+    a.kq = a.nkb / a.ksplit;
+    a.kr = a.nkb % a.ksplit;
     return launch(g, a, blocks, stream);
   };
 #define FP8_SKINNY(NW, MT) run(launch<NW, MT>, Cfg<NW, MT>::THREADS, Cfg<NW, MT>::SMEM)

@@ -12,8 +12,9 @@
 //                      scale found by the two warps that hold the row)
 //   CLUSTERED = true   one output tile per cluster, when there are too few tiles for the SMs: its
 //                      CTAs share out the blocks of K (plain) or the 128 columns of the gated
-//                      pair's scale and then K. Every CTA leaves its sums in shared memory, the
-//                      rows are added up over the cluster, always in the same order.
+//                      pair's scale and then K. Plain: every CTA leaves its sums in shared memory,
+//                      the rows are added up over the cluster, always in the same order. Gated:
+//                      h is made where its sums are, a row's maximum goes round the cluster.
 // Measured (B200): 64 x 8192 x 28672 in 45 us (5.3 TB/s), 64 x 11008 x 4096 in 12.0 us (a loop that
 // only streams this weight: 10.3), 512 x 4096 x 4096 in 12.8 us, gated 100 x 11008 x 4096 in 24.1 us.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-11 epilogue (two per quarter of the TMEM
@@ -35,7 +36,8 @@ constexpr int BM = 128, BK = 128;
 constexpr int THREADS = 384, EPI_WARP0 = 4, N_EPI = 8;
 constexpr int RING_BYTES = 196 * 1024;   // operand ring
 constexpr int MAX_STAGES = 8;
-constexpr int SMEM_BYTES = RING_BYTES + Scales::BYTES + 4 * BM * 4 + 512 + 1024;
+constexpr int STAGE_OUT = 1024;          // staging of one epilogue warp's stores
+constexpr int SMEM_BYTES = RING_BYTES + Scales::BYTES + 4 * BM * 4 + N_EPI * STAGE_OUT + 512 + 1024;
 constexpr uint32_t TMEM_COLS = 512;
 
 struct ThinArgs {
@@ -53,10 +55,42 @@ struct ThinArgs {
   int y_align;        // of the rows of y, in bytes
   int x_rows;         // rows of the X box
   int tiles_n, n_tiles;
-  int ksplit;         // CTAs of a cluster along K
+  int ksplit;         // CTAs of a cluster along K, which have kq stages each, the first kr one more
+  int kq, kr;
   int stages, stage_bytes;
   int32_t* status;
 };
+
+// Rows that 16-byte stores cannot address: 32 bytes of each of the warp's 32 rows, the lane's own being
+// the words get(0) .. get(7), through shared memory, so that a store of the warp covers four rows and not
+// 32 (2000 x 300 x 4096: 19 us with one row a lane, 10.2 so; 300 x 14001 x 512: 13.2).
+template <int ES, typename Get>
+__device__ __forceinline__ void store_rows(const ThinArgs& a, uint32_t st, int row0, int col0, int lane,
+                                           Get get) {
+  auto place = [&](int row, int piece) {  // neither the writes nor the reads conflict
+    return st + (uint32_t)(row * 32 + ((piece ^ ((row >> 2) & 1)) << 4));
+  };
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(place(lane, p)), "r"(get(4 * p)),
+                 "r"(get(4 * p + 1)), "r"(get(4 * p + 2)), "r"(get(4 * p + 3))
+                 : "memory");
+  __syncwarp();
+  const int i = lane & 7;
+  uint32_t w[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    w[r] = gptq::flag_read(place(4 * r + (lane >> 3), i >> 2) + (i & 3) * 4);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[r], 1, 8);
+    const int row = row0 + 4 * r + (lane >> 3);
+    if (row < a.M)
+      gptq::store_word<ES, 8>(reinterpret_cast<uint8_t*>(a.y) + ((long long)row * a.ldy + col0) * ES, i,
+                              w[r], next, a.N - col0);
+  }
+}
 
 struct Maps {  // [0]: whole blocks of K, three-dimensional; [1]: any block, two-dimensional
   CUtensorMap x[2], w0[2], w1[2];
@@ -69,6 +103,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   constexpr int COLS = NW * BN;                                 // TMEM columns of a block of K
   constexpr int KPS = COLS <= 64 ? 4 : COLS <= 128 ? 2 : 1;     // two groups fit in 512 columns
   constexpr int CN = NW == 2 ? 128 / BN : 1;                    // CTAs along the columns of a scale
+  constexpr bool GROUPED = CLUSTERED && NW == 2;                // a cluster holds groups of a scale
   constexpr bool TWO_BLOCKS = 128 % BN != 0;                    // a tile may span two weight blocks
   constexpr int PITCH = BN + 4;                                 // floats; an odd number of 16 bytes
   // 128 sums a thread: the first warpgroup's registers go to the epilogue's, 128 * 56 + 256 * 224 =
@@ -81,8 +116,10 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   const uint32_t smem = (gptq::smem_u32(smem_raw) + 1023u) & ~1023u;
   Scales scales;
   scales.buf = smem + RING_BYTES;
-  const uint32_t amax = scales.buf + Scales::BYTES;  // [2 tiles][2 halves][BM]
-  const uint32_t bars = amax + 4 * BM * 4;
+  // [2 tiles][2 halves][BM], or clustered [BM]
+  const uint32_t amax = scales.buf + Scales::BYTES;
+  const uint32_t out_stage = amax + 4 * BM * 4;
+  const uint32_t bars = out_stage + N_EPI * STAGE_OUT;
   auto full = [&](int s) { return bars + (uint32_t)s * 8; };
   auto empty = [&](int s) { return bars + (uint32_t)(MAX_STAGES + s) * 8; };
   auto acc_full = [&](int b) { return bars + (uint32_t)(2 * MAX_STAGES + b) * 8; };
@@ -95,6 +132,10 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   gptq::let_next_kernel_start();
+  if constexpr (GROUPED) {
+    if (threadIdx.x < BM) gptq::flag_write(amax + threadIdx.x * 4, 0);
+    gptq::cluster_arrive();  // the CTA has started, its maxima are zero
+  }
   if (threadIdx.x == 0) {
     gptq::flag_write(abort_flag, 0);
     for (int s = 0; s < MAX_STAGES; ++s) {
@@ -135,15 +176,22 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   if constexpr (CLUSTERED) {
     asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
     csize = CN * args.ksplit;
-    t0 = blockIdx.x / csize;
+    asm("mov.u32 %0, %clusterid.x;" : "=r"(t0));
     step = args.n_tiles;
     npart = rank % CN;
-    const int ks = rank / CN, groups = (args.nkb + KPS - 1) / KPS;
-    kb0 = groups * ks / args.ksplit * KPS;
-    kb1 = min(args.nkb, groups * (ks + 1) / args.ksplit * KPS);
+    const int ks = rank / CN;
+    kb0 = (ks * args.kq + min(ks, args.kr)) * KPS;
+    kb1 = min(args.nkb, kb0 + (args.kq + (ks < args.kr ? 1 : 0)) * KPS);
   }
   auto row_tile = [&](int t) { return t / args.tiles_n; };
   auto col_of = [&](int t) { return (t % args.tiles_n) * (CN * BN) + npart * BN; };
+
+  // Gated pair in clusters: the barriers that every thread passes, whatever happens to it.
+  auto pass_barriers = [&] {
+    gptq::cluster_wait();
+    if (args.ksplit == 2) gptq::cluster_sync();
+    gptq::cluster_sync();
+  };
 
   if (warp < EPI_WARP0) {
     if constexpr (SPLIT_REGS) gptq::regs_dec<56>();
@@ -254,7 +302,8 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
       }
       Scales::drain();
     }
-    if constexpr (CLUSTERED) {
+    if constexpr (GROUPED) pass_barriers();
+    if constexpr (CLUSTERED && !GROUPED) {
       gptq::cluster_sync();
       gptq::cluster_sync();
     }
@@ -266,7 +315,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
     constexpr int HC = BN / 2;  // columns of a thread, per weight: CH chunks of 16
     int buf = 0, chunk = 0;
     uint32_t acc_phase = 0, tile_parity = 0, chunk_phase = 0;
-    bool ok = !gptq::flag_read(skip_flag), acc_ready = false;
+    bool ok = !gptq::flag_read(skip_flag), acc_ready = false, passed = false;
     for (int t = t0; t < args.n_tiles && ok; t += step) {
       const int row0 = row_tile(t) * BM + quarter * 32, row = row0 + lane;
       const int col0 = col_of(t) + half * HC;
@@ -357,8 +406,86 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
           release();
         }
       }
+      if constexpr (GROUPED) ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      if constexpr (CLUSTERED) {
+      if constexpr (GROUPED) {
+        // Each thread makes h of its own columns; what crosses the cluster is a maximum per row. (The
+        // sums themselves through shared memory, a row at a time: 4400 cycles instead of 1500.)
+        passed = true;
+        const int ks = (int)rank / CN, tid = threadIdx.x - EPI_WARP0 * 32;
+        int first = col0;
+        gptq::cluster_wait();
+        if (args.ksplit == 2) {
+          // Two CTAs hold halves of K: the sums of eight columns each for the other's, by way of the
+          // operand ring, which is free (all MMAs of the CTA are done).
+          const uint32_t slot = smem + (uint32_t)tid * 16;
+#pragma unroll
+          for (int w = 0; w < NW; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(slot + (w * 2 + e / 2) * 4096),
+                           "l"(ks ? acc[w][0][e] : acc[w][0][e + 4]),
+                           "l"(ks ? acc[w][0][e + 1] : acc[w][0][e + 5])
+                           : "memory");
+          gptq::cluster_sync();
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float4 p = gptq::ld_cluster(slot + (w * 2 + e / 2) * 4096, rank ^ CN);
+              acc[w][0][e] = gptq::add2(ks ? acc[w][0][e + 4] : acc[w][0][e], p.x, p.y);
+              acc[w][0][e + 1] = gptq::add2(ks ? acc[w][0][e + 5] : acc[w][0][e + 1], p.z, p.w);
+            }
+#pragma unroll
+            for (int e = 4; e < 8; ++e) acc[w][0][e] = 0ull;
+          }
+          first += 8 * ks;
+        }
+        uint32_t mx = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float h0 = gptq::silu_mul(lo2(acc[0][c][e]), lo2(acc[NW - 1][c][e]));
+            const float h1 = gptq::silu_mul(hi2(acc[0][c][e]), hi2(acc[NW - 1][c][e]));
+            const int col = first + 16 * c + 2 * e;
+            if (col < args.N) mx = max(mx, gptq::mag_bits(h0));
+            if (col + 1 < args.N) mx = max(mx, gptq::mag_bits(h1));
+            asm("mov.b64 %0, {%1, %2};"
+                : "=l"(acc[0][c][e])
+                : "r"(__float_as_uint(h0)), "r"(__float_as_uint(h1)));
+          }
+        const uint32_t slot = amax + (uint32_t)(quarter * 32 + lane) * 4;
+        for (int r = 0; r < csize; ++r) gptq::max_cluster(slot, (uint32_t)r, mx);
+        gptq::cluster_sync();  // behind it a CTA touches its own memory only
+        if (row < args.M) {
+          float s, inv;
+          gptq::block_scale(gptq::flag_read(slot), s, inv);
+          if (rank == 0 && half == 0) args.sy[(long long)row * args.ldsy + col_of(t) / 128] = s;
+          uint8_t* q = reinterpret_cast<uint8_t*>(args.y) + (long long)row * args.ldy + first;
+          const int cols = args.ksplit == 2 ? 8 : 16;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint64_t a = acc[0][c][2 * e], b = acc[0][c][2 * e + 1];
+              o[e] = gptq::e4m3x4(lo2(a) * inv, hi2(a) * inv, lo2(b) * inv, hi2(b) * inv);
+            }
+            const bool whole = first + 16 * c + cols <= args.N && args.y_align >= cols;
+            if (whole && cols == 16) {
+              *reinterpret_cast<uint4*>(q + 16 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else if (whole) {
+              *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (e < cols && first + 16 * c + e < args.N)
+                  q[16 * c + e] = (uint8_t)(o[e >> 2] >> ((e & 3) * 8));
+            }
+          }
+        }
+      } else if constexpr (CLUSTERED) {
         // All MMAs of the CTA are done, so the operand ring is free: the rows' sums.
         if (row < args.M) {
 #pragma unroll
@@ -422,12 +549,29 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
             }
           }
         }
+      } else if (args.y_align < 16) {
+        if (rows_here) {
+          const uint32_t st = out_stage + (uint32_t)(warp - EPI_WARP0) * STAGE_OUT;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            if (args.y_dtype == GPTQ_F32) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                store_rows<4>(args, st, row0, col0 + 16 * c + 8 * h, lane,
+                              [&](int i) { return (uint32_t)(acc[0][c][4 * h + i / 2] >> (i % 2 * 32)); });
+            } else {
+              store_rows<2>(args, st, row0, col0 + 16 * c, lane, [&](int i) {
+                return gptq::pack2(lo2(acc[0][c][i]), hi2(acc[0][c][i]), args.y_dtype);
+              });
+            }
+          }
+        }
       } else if (row < args.M) {
         // 32 or 64 bytes of the row per chunk: whole sectors
         const long long at = (long long)row * args.ldy + col0;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          const bool vec = col0 + 16 * c + 16 <= args.N;  // rows are 16-byte aligned here
+          const bool vec = col0 + 16 * c + 16 <= args.N;
           if (vec && args.y_dtype == GPTQ_F32) {
             float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(args.y) + at + 16 * c);
 #pragma unroll
@@ -456,28 +600,26 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
         }
       }
     }
-    if constexpr (CLUSTERED) {
+    if constexpr (GROUPED) {
+      if (!passed) pass_barriers();
+    } else if constexpr (CLUSTERED) {
       // Every thread of every CTA of the cluster passes both barriers, whatever happened above.
       gptq::cluster_sync();
       if (!gptq::flag_read(skip_flag)) {
-        constexpr int LPR = CN * BN / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+        constexpr int LPR = BN / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp
         const int rows = min(BM, args.M - row_tile(t0) * BM);
-        const int sub = lane / LPR, c4 = (lane % LPR) * 4;
-        const int part = c4 / BN;  // the CTA along the columns that holds them
-        const int tile_col = (t0 % args.tiles_n) * (CN * BN);
+        const int sub = lane / LPR, c4 = (lane % LPR) * 4, tile_col = col_of(t0);
         // Rows are dealt out to the warps of all CTAs in turn, RPW at a time.
         gptq::add_up<NW>(
             (int)rank * N_EPI + warp - EPI_WARP0, csize * N_EPI, (rows + RPW - 1) / RPW, args.ksplit,
-            [&](int w, int r) {
-              return smem + (uint32_t)((w * BM + min(r * RPW + sub, BM - 1)) * PITCH + c4 % BN) * 4;
+            [&](int, int r) {
+              return smem + (uint32_t)(min(r * RPW + sub, BM - 1) * PITCH + c4) * 4;
             },
-            [&](int s) { return (uint32_t)(s * CN + part); },
+            [](int s) { return (uint32_t)s; },
             [&](int r, const float4(&v)[NW]) {
-              const long long row = row_tile(t0) * BM + r * RPW + sub;
               if (sub < RPW && r * RPW + sub < rows)
-                gptq::store_row4<NW>(v, args.y, row * args.ldy, tile_col + c4, args.N, args.y_dtype,
-                                     args.y_align,
-                                     args.sy + (NW == 2 ? row * args.ldsy + tile_col / 128 : 0));
+                gptq::store_row4<NW>(v, args.y, (row_tile(t0) * BM + r * RPW + sub) * args.ldy,
+                                     tile_col + c4, args.N, args.y_dtype, args.y_align, nullptr);
             });
       }
       gptq::cluster_sync();  // no CTA leaves while its sums may still be read
@@ -518,6 +660,8 @@ int launch(const gptq_host::Fp8Gemm& g, ThinArgs a, int sms, cudaStream_t stream
   constexpr int CN = NW == 2 ? 128 / BN : 1;
   const int tiles_m = (g.m + BM - 1) / BM;
   a.tiles_n = (g.n + CN * BN - 1) / (CN * BN);
+  a.kq = (a.nkb + KPS - 1) / KPS / a.ksplit;
+  a.kr = (a.nkb + KPS - 1) / KPS % a.ksplit;
   if ((long long)tiles_m * a.tiles_n > 0x3FFFFFFF) return GPTQ_ERR_CUDA;
   a.n_tiles = tiles_m * a.tiles_n;
   a.stage_bytes = KPS * (a.x_rows + NW * BN) * BK;
@@ -582,7 +726,7 @@ static int resident(int size) {
 long long fp8_thin_cost(const Fp8Gemm& g) {
   const int sms = num_sms();
   if (g.w[1] == nullptr) return tile_cost(g, plain_tile(g, sms), sms);
-  // Gated pair: 32 or 64 rows of each weight where clusters hold all groups (100 x 4096 x 4096: 15.1 us, a
+  // Gated pair: 32 or 64 rows of each weight where clusters hold all groups (100 x 4096 x 4096: 13.1 us, a
   // block 0.33), else 128 (100 x 11008 x 4096: 24.1 us, a block 0.6).
   const long long groups = (long long)((g.m + BM - 1) / BM) * ((g.n + 127) / 128);
   if (groups <= resident(4)) return 195;
@@ -629,14 +773,11 @@ int fp8_thin(const Fp8Gemm& g, cudaStream_t stream) {
       a.ksplit = s;
       return launch<1, 1, true>(g, a, sms, stream);
     }
-  // Rows that 16-byte stores cannot address go out through shared memory, a warp along each row: the
-  // direct stores, one row a lane, took 10 of 19 us at 2000 x 300 x 4096.
-  const bool direct = a.y_align == 16;
   switch (plain_tile(g, sms)) {
-    case 1: return direct ? launch<1, 1, false>(g, a, sms, stream) : launch<1, 1, true>(g, a, sms, stream);
-    case 2: return direct ? launch<1, 2, false>(g, a, sms, stream) : launch<1, 2, true>(g, a, sms, stream);
-    case 3: return direct ? launch<1, 3, false>(g, a, sms, stream) : launch<1, 3, true>(g, a, sms, stream);
-    default: return direct ? launch<1, 4, false>(g, a, sms, stream) : launch<1, 4, true>(g, a, sms, stream);
+    case 1: return launch<1, 1, false>(g, a, sms, stream);
+    case 2: return launch<1, 2, false>(g, a, sms, stream);
+    case 3: return launch<1, 3, false>(g, a, sms, stream);
+    default: return launch<1, 4, false>(g, a, sms, stream);
   }
 }
 

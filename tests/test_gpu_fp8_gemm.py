@@ -41,11 +41,11 @@ def check_rounded(Y, ref, bound, dtype):
     assert np.all(err <= limit[~inf]), float(np.max(err / limit[~inf]))
 
 
-def run_gemm(m, n, k, dtype, seed=0, ldy=None, **kw):
+def run_gemm(m, n, k, dtype, seed=0, ldy=None, offy=0, **kw):
     import post_weight_quantization_18_b200 as G
     X, sx, cx, Sx = operand(m, k, 1, seed + 1, **kw)
     W, sw, cw, Sw = operand(n, k, 128, seed + 2, **kw)
-    Y, raw = padded(m, n, DTYPES[dtype], ld=n if ldy is None else ldy)
+    Y, raw = padded(m, n, DTYPES[dtype], ld=n if ldy is None else ldy, offset=offy)
     st = torch.zeros(2, dtype=torch.int32, device="cuda")
     G.fp8_gemm(X, sx, W, sw, Y, st)
     torch.cuda.synchronize()
@@ -145,6 +145,16 @@ def test_operands_of_any_alignment(m, kw):
 def test_output_pitches(m, dtype, ldy):
     run_gemm(m, 260, 512, dtype, seed=m, ldy=ldy)
     run_gated(m, 260, 512, seed=m, ldq=ldy, offq=ldy % 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("offy", [0, 1, 2, 3, 5])
+@pytest.mark.parametrize("m,n,ldy", [(40, 1, 1), (40, 2, 3), (41, 3, 3), (130, 15, 17), (40, 17, 17),
+                                     (70, 33, 34), (129, 127, 131), (300, 129, 129), (40, 130, 132),
+                                     (1030, 4099, 4099), (1025, 4130, 4134)])
+def test_output_views_of_any_alignment(m, n, ldy, offy, dtype):
+    """Rows that begin at any multiple of the element's size, and end inside a store."""
+    run_gemm(m, n, 136, dtype, seed=m + n, ldy=ldy, offy=offy)
 
 
 def test_scale_pitches_and_stacked_weights():
