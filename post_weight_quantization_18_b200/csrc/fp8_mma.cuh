@@ -265,6 +265,16 @@ GPTQ_DEV void max_cluster(uint32_t saddr, uint32_t rank, uint32_t v) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
+GPTQ_DEV void st_cluster(uint32_t saddr, uint32_t rank, float v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+GPTQ_DEV void st_cluster(uint32_t saddr, uint32_t rank, uint64_t v0, uint64_t v1) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(a), "l"(v0), "l"(v1) : "memory");
+}
 GPTQ_DEV float4 ld_cluster(uint32_t saddr, uint32_t rank) {
   uint32_t a;
   float4 v;
@@ -356,58 +366,6 @@ GPTQ_DEV void store_word(uint8_t* p, int i, uint32_t w, uint32_t next, int left)
     store_if(first ? end > 0 : at + 1 == end, first ? p : q, (uint16_t)(first ? w : v));
     if (end == 2 && first) store_if(true, q, (uint16_t)v);  // both ends are this lane's
   }
-}
-
-// The rows of an output tile, added up over the CTAs of a cluster that shared K, always in their order:
-// rows first, first + stride, ... below `end`, four columns a lane. at(w, r) is the shared-memory
-// address of row r's sums of weight w, who(s) the CTA with part s of K; done(r, v) takes the row (it is
-// called by all lanes). Eight loads are in flight, of one row or of several. Where K was not shared
-// the row is read as the CTA's own memory: by way of the cluster that takes 900 cycles.
-template <int NW, int R, int S, typename At, typename Who, typename Done>
-GPTQ_DEV void add_up_rows(int first, int stride, int end, int ksplit, At at, Who who, Done done) {
-  for (int r0 = first; r0 < end; r0 += R * stride) {
-    float4 p[R][S][NW];
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (s < ksplit) {
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const uint32_t a = at(w, min(r0 + i * stride, end - 1));
-            p[i][s][w] = S == 1 ? lds_f32x4(a) : ld_cluster(a, who(s));
-          }
-        }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (r0 + i * stride >= end) break;
-      float4 v[NW];
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        v[w] = p[i][0][w];
-#pragma unroll
-        for (int s = 1; s < S; ++s)
-          if (s < ksplit) {
-            v[w].x += p[i][s][w].x;
-            v[w].y += p[i][s][w].y;
-            v[w].z += p[i][s][w].z;
-            v[w].w += p[i][s][w].w;
-          }
-      }
-      done(r0 + i * stride, v);
-    }
-  }
-}
-template <int NW, typename At, typename Who, typename Done>
-GPTQ_DEV void add_up(int first, int stride, int end, int ksplit, At at, Who who, Done done) {
-  if (ksplit == 1)
-    add_up_rows<NW, 4, 1>(first, stride, end, ksplit, at, who, done);
-  else if (ksplit == 2)
-    add_up_rows<NW, 4, 2>(first, stride, end, ksplit, at, who, done);
-  else if (ksplit <= 4)
-    add_up_rows<NW, 2, 4>(first, stride, end, ksplit, at, who, done);
-  else
-    add_up_rows<NW, 1, 8>(first, stride, end, ksplit, at, who, done);
 }
 
 }  // namespace gptq

@@ -9,14 +9,14 @@
 //
 // A cluster owns the 128 weight rows of a scale block (gated pair: of both weights); its CTAs share
 // out the blocks of K. The sums of a block are scaled by sx sw in fp32 registers as in fp8_gemm.cu.
-// At the end every CTA leaves its sums in shared memory and each row of the output tile is
-// added up over the cluster, always in the same order, by one warp, which for the gated pair
-// also has the whole 128 columns of the row's scale.
+// At the end the CTAs send one another their sums, each row of the output tile to one of them, where a
+// warp adds them up, always in the same order; for the gated pair it also has the whole 128
+// columns of the row's scale.
 // Two CTAs share an SM, so that one's start and end pass behind the other's stream.
 // Measured (B200): 1 x 8192 x 28672 in 37.3 us (6.3 TB/s, 0.98 of the measured copy rate), 8 x 11008 x
-// 4096 gated in 18.4 us (4.9 TB/s), 64 x 11008 x 4096 gated in 22.0 us, 16 x 11008 x 4096 in 11.0 us (a loop that only streams this
-// weight: 10.3), 1 x 4096 x 4096 in 5.8 us with the weight in L2, of which about 4 are the
-// kernel's start, the latency of its first load and the cluster's exchange.
+// 4096 gated in 18.0 us (5.0 TB/s), 64 x 11008 x 4096 gated in 21.3 us, 16 x 11008 x 4096 in 10.3 us (what
+// a loop that only streams this weight takes), 1 x 4096 x 4096 in 6.0 us, of which more than 3 are
+// the kernel's start, the latency of its first load and the cluster's exchange.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-7 epilogue (gated pair: 8-11 the
 // second weight's). Every wait is bounded as in fp8_gemm.cu.
 #include "fp8_mma.cuh"
@@ -28,7 +28,6 @@ using gptq::bar_wait_rest;
 
 constexpr int BM = 128, BK = 128;
 constexpr int W_TILE = BM * BK;  // 16 KB
-constexpr int PITCH = BM + 4;    // floats of a row of sums
 constexpr int EPI_WARP0 = 4;
 
 template <int NW, int MT>
@@ -39,13 +38,18 @@ struct Cfg {
   static constexpr int CTAS_PER_SM = NW * MT > 64 ? 1 : 2;
   static constexpr int NBUF = 4;  // accumulators
   static constexpr int STAGE_BYTES = NW * W_TILE + MT * BK;
-  static constexpr int STAGES = (CTAS_PER_SM == 2 ? 102 : 204) * 1024 / STAGE_BYTES;
+  // Where the cluster's sums arrive: the CTA's share of the rows times the CTAs, 36 of 32 at seven. The
+  // plain product has room for it beside the ring, the gated pair uses the ring again.
+  static constexpr bool APART = NW == 1;
+  static constexpr int SUMS = (MT + 5) * NW * BM * 4, RECV = APART ? SUMS : 0;
+  static constexpr int STAGES = 
+      (228 * 1024 / CTAS_PER_SM - 1024 - 1024 - 512 - RECV - Scales::BYTES) / STAGE_BYTES;
   static constexpr int RING = STAGES * STAGE_BYTES;
-  static constexpr int SMEM = RING + Scales::BYTES + 512 + 1024;
+  static constexpr int SMEM = RING + RECV + Scales::BYTES + 512 + 1024;
   static constexpr uint32_t TMEM_COLS = NBUF * NW * MT;  // 64 to 512
   static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024 && STAGES >= 2, "shared memory");
   static_assert(CTAS_PER_SM * TMEM_COLS <= 512, "tensor memory");
-  static_assert(NW * MT * PITCH * 4 <= RING, "sums");
+  static_assert(APART || SUMS <= RING, "sums");
 };
 
 struct SkinnyArgs {
@@ -76,7 +80,8 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (gptq::smem_u32(smem_raw) + 1023u) & ~1023u;
   Scales scales;
-  scales.buf = smem + C::RING;
+  const uint32_t recv = C::APART ? smem + C::RING : smem;
+  scales.buf = smem + C::RING + C::RECV;
   const uint32_t bars = scales.buf + Scales::BYTES;
   auto full = [&](int s) { return bars + (uint32_t)s * 8; };
   auto empty = [&](int s) { return bars + (uint32_t)(C::STAGES + s) * 8; };
@@ -92,6 +97,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   asm("mov.u32 %0, %clusterid.x;" : "=r"(cluster_id));
 
   gptq::let_next_kernel_start();
+  if constexpr (C::APART) gptq::cluster_arrive();  // the CTA has started
   if (threadIdx.x == 0) {
     gptq::flag_write(abort_flag, 0);
     for (int s = 0; s < C::STAGES; ++s) {
@@ -127,6 +133,14 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   const int block = (int)cluster_id;
   const int kb0 = (int)rank * args.kq + min((int)rank, args.kr);
   const int kb1 = kb0 + args.kq + ((int)rank < args.kr ? 1 : 0);
+
+  // Every thread of every CTA of the cluster passes this barrier and the next, whatever happens to it.
+  auto ready_to_receive = [&] {
+    if constexpr (C::APART)
+      gptq::cluster_wait();  // all CTAs have started
+    else
+      gptq::cluster_sync();  // all MMAs of all CTAs are done
+  };
 
   if (warp < EPI_WARP0) {
     if (skip) {
@@ -196,7 +210,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                      abort_flag);
       Scales::drain();
     }
-    gptq::cluster_sync();
+    ready_to_receive();
     gptq::cluster_sync();
   } else {
     // ---------------- epilogue: one weight row a thread ----------------
@@ -254,31 +268,58 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         if (++chunk == Scales::CHUNKS) { chunk = 0; chunk_phase ^= 1; }
       }
     }
-    // All MMAs of the CTA are done, so the operand ring is free: rows of 128 sums.
-    if (ok) {
+    // Rows are dealt out to the CTAs, each of which gets ksplit sums of its rows, side by side. They are
+    // sent and not fetched: a load from another CTA takes 900 cycles, and so does the barrier that
+    // keeps a CTA until the others have loaded (1 x 2048 x 4096: 5.55 us so, 4.5 sent).
+    ready_to_receive();
+    const uint32_t mine = recv + (rank * NW + w) * (BM * 4) + (uint32_t)(quarter * 32 + lane) * 4;
+    auto sum = [&](int c) { return c & 1 ? gptq::hi2(acc[c / 2]) : gptq::lo2(acc[c / 2]); };
+    if (ok && args.ksplit == 1) {
 #pragma unroll
       for (int c = 0; c < MT; ++c)
         if (c < args.M)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(
-                           smem + (uint32_t)((w * MT + c) * PITCH + quarter * 32 + lane) * 4),
-                       "f"(c & 1 ? gptq::hi2(acc[c / 2]) : gptq::lo2(acc[c / 2]))
-                       : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + c * (NW * BM * 4)), "f"(sum(c)) : "memory");
+    } else if (ok) {
+      uint32_t at = mine;
+      int to = 0;
+#pragma unroll
+      for (int c = 0; c < MT; ++c)
+        if (c < args.M) {
+          gptq::st_cluster(at, (uint32_t)to, sum(c));
+          if (++to == args.ksplit) {
+            to = 0;
+            at += (uint32_t)(NW * BM * 4) * args.ksplit;
+          }
+        }
     }
-    // Every thread of every CTA of the cluster passes both barriers, whatever happened above.
-    gptq::cluster_sync();
-    if (!skip) {
-      // Rows are dealt out to the warps of all CTAs in turn.
-      gptq::add_up<NW>(
-          (int)rank * 4 * NW + warp - EPI_WARP0, args.ksplit * 4 * NW, args.M, args.ksplit,
-          [&](int i, int r) { return smem + (uint32_t)((i * MT + r) * PITCH + lane * 4) * 4; },
-          [](int s) { return (uint32_t)s; },
-          [&](int r, const float4(&v)[NW]) {
-            gptq::store_row4<NW>(v, args.y, (long long)r * args.ldy, block * 128 + lane * 4, args.N,
-                                 args.y_dtype, args.y_align,
-                                 args.sy + (NW == 2 ? (long long)r * args.ldsy + block : 0));
-          });
+    gptq::cluster_sync();  // behind it a CTA touches its own memory only
+    // A warp a row, four columns a lane; the parts of K are added up in their order.
+    for (int i = warp - EPI_WARP0; !skip; i += 4 * NW) {
+      const int r = (int)rank + i * args.ksplit;
+      if (r >= args.M) break;
+      const uint32_t from = recv + (uint32_t)(i * args.ksplit * NW * BM + lane * 4) * 4;
+      float4 p[8][NW];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < args.ksplit) {
+#pragma unroll
+          for (int j = 0; j < NW; ++j) p[s][j] = gptq::lds_f32x4(from + (s * NW + j) * (BM * 4));
+        }
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < args.ksplit) {
+#pragma unroll
+          for (int j = 0; j < NW; ++j) {
+            p[0][j].x += p[s][j].x;
+            p[0][j].y += p[s][j].y;
+            p[0][j].z += p[s][j].z;
+            p[0][j].w += p[s][j].w;
+          }
+        }
+      gptq::store_row4<NW>(p[0], args.y, (long long)r * args.ldy, block * 128 + lane * 4, args.N,
+                           args.y_dtype, args.y_align,
+                           args.sy + (NW == 2 ? (long long)r * args.ldsy + block : 0));
     }
-    gptq::cluster_sync();  // no CTA leaves while its sums may still be read
   }
 
   gptq::tc_fence_before();
@@ -334,10 +375,16 @@ int fp8_skinny(const Fp8Gemm& g, cudaStream_t stream) {
   const int es = gated ? 1 : g.y_dtype == GPTQ_F32 ? 4 : 2;
   a.y_align = row_align(g.y, g.ldy * es);
   const int blocks = (g.n + BM - 1) / BM;
-  // As many CTAs along K as clusters of them are resident at once, each with four blocks of K at least.
+  // As many CTAs along K as clusters of them are resident at once, each with four blocks of K at least;
+  // large clusters with room to spare, since the last ones start late (1 x 4096 x 4096 in 32 clusters
+  // of 8 of the 33 there are: 6.8 us, of 7: 6.3, of 6: 6.0; 1 x 8192 x 8192 in 64 of 4 of 71: 14.2, of 3:
+  // 13.4; but 16 x 11008 x 4096 in 86 of 3: 10.3, of 2: 11.6; gated 1 x 4096 x 4096 of 7: 9.5, of 6: 9.8).
   auto run = [&](auto launch, int threads, int smem) {
     a.ksplit = a.nkb >= 32 ? 8 : a.nkb >= 8 ? a.nkb / 4 : 1;
-    while (a.ksplit > 1 && blocks > resident_clusters(threads, smem, a.ksplit)) --a.ksplit;
+    auto fits = [&](int s) {
+      return blocks + (s > 3 ? blocks / (gated ? 8 : 4) : 0) <= resident_clusters(threads, smem, s);
+    };
+    while (a.ksplit > 1 && !fits(a.ksplit)) --a.ksplit;
     a.kq = a.nkb / a.ksplit;
     a.kr = a.nkb % a.ksplit;
     return launch(g, a, blocks, stream);

@@ -12,8 +12,8 @@
 //                      scale found by the two warps that hold the row)
 //   CLUSTERED = true   one output tile per cluster, when there are too few tiles for the SMs: its
 //                      CTAs share out the blocks of K (plain) or the 128 columns of the gated
-//                      pair's scale and then K. Plain: every CTA leaves its sums in shared memory,
-//                      the rows are added up over the cluster, always in the same order. Gated:
+//                      pair's scale and then K. Plain: the sums of a row are sent to one of them
+//                      and added up there, always in the same order. Gated:
 //                      h is made where its sums are, a row's maximum goes round the cluster.
 // Measured (B200): 64 x 8192 x 28672 in 45 us (5.3 TB/s), 64 x 11008 x 4096 in 12.0 us (a loop that
 // only streams this weight: 10.3), 512 x 4096 x 4096 in 12.8 us, gated 100 x 11008 x 4096 in 24.1 us.
@@ -110,7 +110,8 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   // 384 * 168 as in fp8_gemm.cu
   constexpr bool SPLIT_REGS = NW * CH == 8;
   static_assert(NW == 1 || CN * BN == 128, "the gated pair's tiles divide a scale's columns");
-  static_assert(NW * BM * PITCH * 4 <= RING_BYTES, "partial sums");
+  static_assert(!CLUSTERED || GROUPED || CH == 1, "sixteen columns a thread");
+  static_assert((BM + 7) * PITCH * 4 <= RING_BYTES, "partial sums");
   constexpr uint32_t IDESC = gptq::instr_desc(/*e4m3*/ 0, 0, 0, BM, BN);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = (gptq::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -186,10 +187,10 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   auto row_tile = [&](int t) { return t / args.tiles_n; };
   auto col_of = [&](int t) { return (t % args.tiles_n) * (CN * BN) + npart * BN; };
 
-  // Gated pair in clusters: the barriers that every thread passes, whatever happens to it.
+  // In clusters: the barriers that every thread passes, whatever happens to it.
   auto pass_barriers = [&] {
-    gptq::cluster_wait();
-    if (args.ksplit == 2) gptq::cluster_sync();
+    if constexpr (GROUPED) gptq::cluster_wait();
+    if (!GROUPED || args.ksplit == 2) gptq::cluster_sync();
     gptq::cluster_sync();
   };
 
@@ -302,11 +303,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
       }
       Scales::drain();
     }
-    if constexpr (GROUPED) pass_barriers();
-    if constexpr (CLUSTERED && !GROUPED) {
-      gptq::cluster_sync();
-      gptq::cluster_sync();
-    }
+    if constexpr (CLUSTERED) pass_barriers();
   } else {
     // ---------------- epilogue ----------------
     if constexpr (SPLIT_REGS) gptq::regs_inc<224>();
@@ -406,7 +403,7 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
           release();
         }
       }
-      if constexpr (GROUPED) ok = __all_sync(0xFFFFFFFFu, ok);
+      if constexpr (CLUSTERED) ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       if constexpr (GROUPED) {
         // Each thread makes h of its own columns; what crosses the cluster is a maximum per row. (The
@@ -486,20 +483,38 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
           }
         }
       } else if constexpr (CLUSTERED) {
-        // All MMAs of the CTA are done, so the operand ring is free: the rows' sums.
+        // Rows are dealt out to the CTAs, each of which gets the parts of its rows side by side in its
+        // operand ring. They are sent, not fetched: a load from another CTA takes 900 cycles, and so does
+        // the barrier that keeps a CTA until the others have loaded.
+        passed = true;
+        gptq::cluster_sync();  // all MMAs of all CTAs are done
+        const int r = quarter * 32 + lane, ks = args.ksplit;
         if (row < args.M) {
+          const uint32_t to = smem + (uint32_t)((r / ks * ks + (int)rank) * PITCH + half * HC) * 4;
 #pragma unroll
-          for (int w = 0; w < NW; ++w)
+          for (int e = 0; e < 4; ++e)
+            gptq::st_cluster(to + 16 * e, (uint32_t)(r % ks), acc[0][0][2 * e], acc[0][0][2 * e + 1]);
+        }
+        gptq::cluster_sync();  // behind it a CTA touches its own memory only
+        // Eight lanes a row, four columns each; the parts are added up in their order.
+        const int rows = min(BM, args.M - row_tile(t) * BM), c4 = (lane & 7) * 4;
+        for (int i = (warp - EPI_WARP0) * 4 + (lane >> 3); (int)rank + i * ks < rows; i += 4 * N_EPI) {
+          const uint32_t from = smem + (uint32_t)(i * ks * PITCH + c4) * 4;
+          float4 p[8], v[NW];
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              const uint32_t p = smem + (uint32_t)((w * BM + quarter * 32 + lane) * PITCH +
-                                                   half * HC + 16 * c) * 4;
+          for (int j = 0; j < 8; ++j)
+            if (j < ks) p[j] = gptq::lds_f32x4(from + j * PITCH * 4);
+          v[0] = p[0];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(p + 16 * e),
-                             "l"(acc[w][c][2 * e]), "l"(acc[w][c][2 * e + 1])
-                             : "memory");
+          for (int j = 1; j < 8; ++j)
+            if (j < ks) {
+              v[0].x += p[j].x;
+              v[0].y += p[j].y;
+              v[0].z += p[j].z;
+              v[0].w += p[j].w;
             }
+          gptq::store_row4<NW>(v, args.y, (row_tile(t) * BM + (long long)rank + i * ks) * args.ldy,
+                               tile_col + c4, args.N, args.y_dtype, args.y_align, nullptr);
         }
       } else if constexpr (NW == 2) {
         // h over the thread's 64 columns; the row's maximum with the warp of the other half.
@@ -600,30 +615,8 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
         }
       }
     }
-    if constexpr (GROUPED) {
+    if constexpr (CLUSTERED)
       if (!passed) pass_barriers();
-    } else if constexpr (CLUSTERED) {
-      // Every thread of every CTA of the cluster passes both barriers, whatever happened above.
-      gptq::cluster_sync();
-      if (!gptq::flag_read(skip_flag)) {
-        constexpr int LPR = BN / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp
-        const int rows = min(BM, args.M - row_tile(t0) * BM);
-        const int sub = lane / LPR, c4 = (lane % LPR) * 4, tile_col = col_of(t0);
-        // Rows are dealt out to the warps of all CTAs in turn, RPW at a time.
-        gptq::add_up<NW>(
-            (int)rank * N_EPI + warp - EPI_WARP0, csize * N_EPI, (rows + RPW - 1) / RPW, args.ksplit,
-            [&](int, int r) {
-              return smem + (uint32_t)(min(r * RPW + sub, BM - 1) * PITCH + c4) * 4;
-            },
-            [](int s) { return (uint32_t)s; },
-            [&](int r, const float4(&v)[NW]) {
-              if (sub < RPW && r * RPW + sub < rows)
-                gptq::store_row4<NW>(v, args.y, (row_tile(t0) * BM + r * RPW + sub) * args.ldy,
-                                     tile_col + c4, args.N, args.y_dtype, args.y_align, nullptr);
-            });
-      }
-      gptq::cluster_sync();  // no CTA leaves while its sums may still be read
-    }
   }
 
   gptq::tc_fence_before();
