@@ -213,7 +213,10 @@ template <typename... P, typename... A>
 int fp8_launch(void (*kernel)(P...), long long grid, int threads, int smem, int cluster,
                cudaStream_t stream, const A&... args) {
   if (grid < 1 || grid > 0x7FFFFFFFll) return GPTQ_ERR_CUDA;
-  if (smem > 48 * 1024 && ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem) != 0)
+  // 48 KB are open to every kernel, its static shared memory included. 64 KB at least are asked for, so that
+  // a kernel whose need grows with its rows (the norm: up to that) is asked for once.
+  const int most = smem < 64 * 1024 ? 64 * 1024 : smem;
+  if (smem > 47 * 1024 && ensure_smem_attr(reinterpret_cast<const void*>(kernel), most) != 0)
     return GPTQ_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
