@@ -234,10 +234,11 @@ __device__ __forceinline__ float inv_rms(float sum, const NormArgs& a) {
 // and so are rows of fp32, of whose sectors a thread's two copies would each fetch all (67 us
 // at 4096 x 5120, loaded 55).
 template <typename T, typename TG, int V, bool TEAM_WARP>
-__global__ void __launch_bounds__(512) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(512, V == 4 ? 2 : 1) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   constexpr bool AHEAD = sizeof(T) == 2;
-  // gamma before the row's sum, but not where a CTA has one row only and the registers are short
-  constexpr bool EARLY = AHEAD || V == 1;
+  // gamma before the row's sum, but not where registers are short: with four vectors they are better
+  // spent on a second CTA (8192 x 8704 of bf16: 137 us, so 97)
+  constexpr bool EARLY = (AHEAD && V < 4) || V == 1;
   extern __shared__ __align__(16) uint8_t next_row[];  // [x, r][V][threads] of 16 bytes
   __shared__ float part[2][32];
   gptq::let_next_kernel_start();
@@ -378,13 +379,14 @@ int launch_norm(NormArgs a, cudaStream_t stream) {
   const int vecs = (a.k + 7) / 8;
   // A warp per row while a row fits in two vectors a lane; then a CTA, of up to 512 threads. As many
   // CTAs as the SMs hold, all rows dealt out to them (2048 threads an SM: 52 us at 8192 x 5120 of
-  // bf16, 1536: 55; 640 threads a row instead of 320: 69). Rows of fp32, which nothing fetches ahead,
+  // bf16, 1536: 55; 640 threads a row instead of 320: 69; with four vectors a thread 1024: 77 us at
+  // 6000 x 10240 and 75 at 8192 x 7168, 1536: 92 and 84, 2048: 77 and 79). Rows of fp32, which nothing fetches ahead,
   // get a CTA each (55 us at 4096 x 5120, dealt out 68).
   auto run = [&](auto kernel, int v, bool team_warp) {
     const int threads = team_warp ? 256 : ((vecs + v - 1) / v + 31) / 32 * 32;
     const int teams = team_warp ? threads / 32 : 1;
     const long long ctas = ((long long)a.m + teams - 1) / teams;
-    const long long most = (long long)gptq_host::num_sms() * (2048 / threads);
+    const long long most = (long long)gptq_host::num_sms() * ((v == 4 ? 1024 : 2048) / threads);
     return fp8_launch(kernel, sizeof(T) == 4 || ctas < most ? ctas : most, threads,
                       sizeof(T) == 2 ? 2 * v * threads * 16 : 0, 1, stream, a);
   };

@@ -182,6 +182,30 @@ def test_norm_any_alignment(off, ld):
     assert untouched(raw_h, H) and untouched(raw_q, Q)
 
 
+@pytest.mark.parametrize("off,ld", [(0, 1004), (4, 1008), (8, 1000), (2, 1002), (1, 1001)])
+@pytest.mark.parametrize("k", [1000, 997])
+def test_fp32_rows_of_any_alignment(off, ld, k):
+    """Rows that start at 4, 8, 16 or 32 bytes, or at these in turn."""
+    import post_weight_quantization_18_b200 as G
+    m = 9
+    X, R, gamma = _norm_case(m, k, "fp32", "fp32", 6)
+    x, _ = padded(m, k, torch.float32, ld=ld, offset=off)
+    x.copy_(X)
+    H, raw_h = padded(m, k, torch.float32, ld=ld, offset=off)
+    Q, raw_q = padded(m, k, torch.uint8, ld=1008)
+    S = torch.empty((m, 8), device="cuda")
+    G.fp8_add_rmsnorm(x, R.cuda(), gamma.cuda(), 1e-5, H, Q, S)
+    _check_norm(X, R, gamma, np.float32(1e-5), H, Q, S, "fp32")
+    assert untouched(raw_h, H) and untouched(raw_q, Q)
+    for rows in (1, 128):
+        S = torch.empty((-(-m // rows), 8), device="cuda")
+        G.fp8_quantize(x, Q, S, rows)
+        codes, scales = o.quantize(X.numpy(), rows)
+        np.testing.assert_array_equal(S.cpu().numpy(), scales)
+        np.testing.assert_array_equal(codes_of(Q), codes)
+    assert untouched(raw_q, Q)
+
+
 def test_norm_zero_rows_and_nonfinite():
     """A row of zeros: y = 0, scales 1. With eps = 0 it is 0 / 0, as the formula says. A NaN or an
     infinity makes NaN what it reaches and leaves the other rows alone."""
