@@ -45,7 +45,7 @@ namespace gptq_host {
 
 int resident_clusters(int threads, int smem, int size) {
   struct Entry { int threads, smem, dev, size, count; };
-  static Entry known[64];
+  static Entry known[512];  // five kernels of few rows and one more, sizes 2 to 8, a device
   static int n_known = 0;
   static std::mutex mu;
   int dev = 0;
@@ -71,7 +71,7 @@ int resident_clusters(int threads, int smem, int size) {
     (void)cudaGetLastError();
     count = 0;
   }
-  if (n_known < 64) known[n_known++] = Entry{threads, smem, dev, size, count};
+  if (n_known < 512) known[n_known++] = Entry{threads, smem, dev, size, count};
   return count;
 }
 
