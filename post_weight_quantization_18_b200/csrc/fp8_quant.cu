@@ -234,7 +234,7 @@ __device__ __forceinline__ float inv_rms(float sum, const NormArgs& a) {
 // and so are rows of fp32, of whose sectors a thread's two copies would each fetch all (67 us
 // at 4096 x 5120, loaded 55).
 template <typename T, typename TG, int V, bool TEAM_WARP>
-__global__ void __launch_bounds__(512, V == 4 ? 2 : 1) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(512, 2) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   constexpr bool AHEAD = sizeof(T) == 2;
   // gamma before the row's sum, but not where registers are short: with four vectors they are better
   // spent on a second CTA (8192 x 8704 of bf16: 137 us, so 97)
