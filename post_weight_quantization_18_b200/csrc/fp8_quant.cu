@@ -378,15 +378,15 @@ int launch_norm(NormArgs a, cudaStream_t stream) {
   using gptq_host::fp8_launch;
   const int vecs = (a.k + 7) / 8;
   // A warp per row while a row fits in two vectors a lane; then a CTA, of up to 512 threads. As many
-  // CTAs as the SMs hold, all rows dealt out to them (2048 threads an SM: 52 us at 8192 x 5120 of
-  // bf16, 1536: 55; 640 threads a row instead of 320: 69; with four vectors a thread 1024: 77 us at
-  // 6000 x 10240 and 75 at 8192 x 7168, 1536: 92 and 84, 2048: 77 and 79). Rows of fp32, which nothing fetches ahead,
-  // get a CTA each (55 us at 4096 x 5120, dealt out 68).
+  // CTAs as the SMs hold, which is 1024 threads with 64 registers, all rows dealt out to them (8192 x
+  // 3584 of bf16 38.8 us, 8192 x 5120 53.2, 8192 x 7168 75; 1536 threads: 42.1, 56.1, 84; 2048: 41.3,
+  // 52.8, 79; 640 threads a row instead of 320 took 69 at 8192 x 5120). Rows of fp32, which nothing
+  // fetches ahead, get a CTA each (55 us at 4096 x 5120, dealt out 68).
   auto run = [&](auto kernel, int v, bool team_warp) {
     const int threads = team_warp ? 256 : ((vecs + v - 1) / v + 31) / 32 * 32;
     const int teams = team_warp ? threads / 32 : 1;
     const long long ctas = ((long long)a.m + teams - 1) / teams;
-    const long long most = (long long)gptq_host::num_sms() * ((v == 4 ? 1024 : 2048) / threads);
+    const long long most = (long long)gptq_host::num_sms() * (1024 / threads);
     return fp8_launch(kernel, sizeof(T) == 4 || ctas < most ? ctas : most, threads,
                       sizeof(T) == 2 ? 2 * v * threads * 16 : 0, 1, stream, a);
   };
