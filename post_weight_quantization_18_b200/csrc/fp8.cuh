@@ -178,6 +178,22 @@ GPTQ_DEV Vec8<T> load8(const T* p, int valid, bool vec) {
       const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
       v.w[i] = q.x; v.w[i + 1] = q.y; v.w[i + 2] = q.z; v.w[i + 3] = q.w;
     }
+  } else if (sizeof(T) == 2 && valid == 8) {
+    // Whole words (norm of 8192 x 4097: 97 us, with 2-byte loads and stores 143), and an element at
+    // either end where p is between two.
+    const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+    if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    } else {
+      uint32_t last = e[0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t next = i < 3 ? *reinterpret_cast<const uint32_t*>(e + 1 + 2 * i) : e[7];
+        v.w[i] = last | (next << 16);
+        last = next >> 16;
+      }
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -195,6 +211,18 @@ GPTQ_DEV void store8(T* p, const Vec8<T>& v, int valid, bool vec) {
     for (int i = 0; i < Vec8<T>::kWords; i += 4)
       *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) =
           make_uint4(v.w[i], v.w[i + 1], v.w[i + 2], v.w[i + 3]);
+  } else if (sizeof(T) == 2 && valid == 8) {
+    uint16_t* e = reinterpret_cast<uint16_t*>(p);
+    if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(p)[i] = v.w[i];
+    } else {
+      e[0] = (uint16_t)v.w[0];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<uint32_t*>(e + 1 + 2 * i) = (v.w[i] >> 16) | (v.w[i + 1] << 16);
+      e[7] = (uint16_t)(v.w[3] >> 16);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
