@@ -283,3 +283,62 @@ def test_binding_refuses_mixed_tensors():
     with pytest.raises(G.GPTQError) as e:                 # rows that overlap
         G.fp8_quantize(X[:1].expand(4, 256), Q, S)
     assert e.value.code == 1
+
+
+# (width, what takes it): a warp a row with one and two vectors, a CTA with one, two and four, long rows.
+NORM_FORMS = [200, 500, 2048, 5120, 12288, 20000]
+
+
+def _check_norm_small(X, gamma, eps, Q, S):
+    """As _check_norm, with the spacing of subnormal numbers: h / rms is off by half of it, times gamma,
+    and y by another half."""
+    g = f64(gamma)
+    _, y = o.add_rmsnorm(f64(X), None, g, eps)
+    dy = np.abs(y) * NORM_REL + 2.0 ** -150 * (1 + np.abs(g))
+    check_format(codes_of(Q), S.cpu().numpy(), y, dy)
+
+
+@pytest.mark.parametrize("dtype,gdtype", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("k", NORM_FORMS)
+def test_norm_blocks_of_very_small_values(k, dtype, gdtype):
+    """Zeros beside values for which 1 / s is large, at a 1 / rms of 1 to 316: every scale is finite, so no
+    code may be NaN, and the zeros stay zeros."""
+    import post_weight_quantization_18_b200 as G
+    m = 4
+    X = _values(m, k, k, dtype)
+    X[0, :128] = 0
+    X[0, 3], X[0, 4] = 1e-36, 5e-37                       # in a row of ordinary values
+    X[1] = 0
+    X[1, ::3] = 1e-37                                     # a whole row: 1 / rms = 1 / sqrt(eps)
+    X[1, 1::7] = -3e-38
+    X[2] = (X[2].float() * 0.01).to(X.dtype)
+    X[2, 128:] = 0
+    X[2, 130::5] = 2.0 ** -130                            # subnormal in every type here
+    gamma = torch.ones(k).to(DTYPES[gdtype])
+    Q = torch.empty((m, k), dtype=torch.uint8, device="cuda")
+    S = torch.empty((m, -(-k // 128)), device="cuda")
+    G.fp8_add_rmsnorm(X.cuda(), None, gamma.cuda(), 1e-5, None, Q, S)
+    assert torch.isfinite(S).all() and not ((Q & 0x7F) == 0x7F).any()
+    assert not (Q.cpu()[X == 0] & 0x7F).any()
+    _check_norm_small(X, gamma, np.float32(1e-5), Q, S)
+
+
+@pytest.mark.parametrize("dtype,gdtype", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("k", NORM_FORMS)
+def test_norm_takes_gamma_after_the_mean(k, dtype, gdtype):
+    """y is an ordinary number although h gamma is none: gamma beyond 1e19 with large h, far below 1 with
+    small h. bf16 and fp32 rows of all sizes; of fp16 the ordinary ones."""
+    import post_weight_quantization_18_b200 as G
+    size = (1.0, 1.0, 1.0) if dtype == "fp16" else (1e16, 1.0, 1e-18)
+    m = 3
+    X = _values(m, k, k + 1, "fp32").clamp(-4, 4)
+    X = (X * torch.tensor(size)[:, None]).to(DTYPES[dtype])
+    gamma = torch.ones(k)
+    gamma[:60] = 1e25
+    gamma[128:] = 1e-27
+    gamma = gamma.to(DTYPES[gdtype])
+    Q = torch.empty((m, k), dtype=torch.uint8, device="cuda")
+    S = torch.empty((m, -(-k // 128)), device="cuda")
+    G.fp8_add_rmsnorm(X.cuda(), None, gamma.cuda(), 1e-37, None, Q, S)
+    assert torch.isfinite(S).all()
+    _check_norm_small(X, gamma, np.float32(1e-37), Q, S)
