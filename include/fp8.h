@@ -101,6 +101,7 @@ int fp8_gemm(const uint8_t* X, int64_t ldx, const float* sx, int64_t ldsx, const
  * fp8_gated_gemm — the gated pair of products of a feed-forward block, from the format to the
  * format:
  *   g = X Wg^T, u = X Wu^T (as fp8_gemm, kept in fp32), h = g / (1 + exp(-g)) * u
+ *   (the sigmoid in fp32: a subnormal number for g below -87.3, zero below -104)
  *   Q, scales = h in the format, one scale per row and 128 columns
  *
  *   X, sx       as in fp8_gemm

@@ -314,3 +314,42 @@ def test_binding_refuses_wrong_operands():
         G.fp8_gemm(q, s, q, sw, torch.zeros((4, 4), device="cuda").t())
     with pytest.raises(ValueError, match=r"Q must be \[4, 4\]"):
         G.fp8_gated_gemm(q, s, q, sw, q, sw, q, s)
+
+
+# Gates around the points where exp(-g) passes 2^126 (-87.34), 2^128 (-88.72) and, as exp(g), the smallest
+# subnormal number (-103.97), around -64 and 0.
+GATES = [-150.0, -120.0, -104.5, -103.9, -100.0, -95.0, -89.0, -88.75, -88.7, -88.5, -88.0, -87.5, -87.375,
+         -87.25, -87.0, -80.0, -64.5, -64.0, -63.5, -40.0, -1.0, -0.5, 0.25, 3.0, 30.0, 87.0, 88.0, 89.0]
+
+
+@pytest.mark.parametrize("m,n,ld", [
+    (10, 200, 16), (28, 130, 16), (60, 4864, 16),         # few rows: 16, 32, 64 of them a tile
+    (100, 300, 16), (100, 6144, 16), (100, 11008, 16),    # tiles of 32, 64 and 128 weight rows
+    (300, 4096, 16), (40, 130, 17),                       # pairs of CTAs; operands TMA cannot address
+])
+def test_gate_far_below_zero(m, n, ld):
+    """silu(g) u with g of -150 to 89, exact in the sums, and u so large that h is an ordinary number: one
+    column of K, x = 1 with the scale |g|, Wg = -1 or 1, and Wu = the e4m3 numbers with the scale 2^100.
+    The sigmoid e / (1 + e), e = exp(g), is off by 9 * 2^-24 of itself (exp 2 ulp, of 2^-23 at most: 4; the sum
+    1, the quotient of 2 ulp 4) and, being a subnormal number from -87.3 on, by 2 ulp of exp and 1 of the
+    quotient, 2^-149 each: 2^-147 at most. Two products and u itself: 3 * 2^-24."""
+    import post_weight_quantization_18_b200 as G
+    gates = np.resize(np.array(GATES, np.float32), m)
+    for sign in (-1, 1):
+        rows = np.where(np.sign(gates) == sign, gates, np.float32(sign))
+        buf = lambda r: padded(r, 1, torch.uint8, ld=ld)[0]
+        X, Wg, Wu = buf(m), buf(n), buf(n)
+        X.fill_(0x38)                                     # 1
+        Wg.fill_(0x38 if sign > 0 else 0xB8)
+        codes = np.resize(np.arange(1, 127, dtype=np.uint8), n)
+        codes[1::2] |= 0x80
+        Wu.copy_(torch.from_numpy(codes)[:, None])
+        sx = torch.from_numpy(np.abs(rows))[:, None].cuda()
+        sg = torch.ones((-(-n // 128), 1), device="cuda")
+        out = G.fp8.empty(m, n)
+        G.fp8_gated_gemm(X, sx, Wg, sg, Wu, sg * 2.0 ** 100, out.q, out.scales)
+        g = rows.astype(np.float64)[:, None]
+        u = np.abs(g) * o.decode(codes)[None] * 2.0 ** 100
+        h = g * u / (1 + np.exp(-g))
+        dh = np.abs(h) * 12 * 2.0 ** -24 + np.abs(g * u) * 2.0 ** -147
+        check_format(codes_of(out.q), out.scales.cpu().numpy(), h, dh)
