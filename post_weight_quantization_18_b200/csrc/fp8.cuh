@@ -18,7 +18,8 @@ constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: 1 / s stays finite
 // runs (fp8_launch): they set up what is their own, then wait for that kernel and its writes. Every
 // thread calls this before it reads or writes memory that a caller owns.
 GPTQ_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel in the stream start (it waits as above).
+// Lets the next kernel in the stream start (it waits as above), once every CTA has a thread that came here. A
+// kernel that needs tensor memory has it by then: otherwise the next one could take an SM's and wait.
 GPTQ_DEV void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

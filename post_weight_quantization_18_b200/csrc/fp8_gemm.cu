@@ -217,7 +217,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   uint32_t rank;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
 
-  gptq::let_next_kernel_start();
   if (threadIdx.x == 0) {
     gptq::flag_write(abort_flag, 0);
     for (int s = 0; s < STAGES; ++s) {
@@ -241,6 +240,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                  "r"(TMEM_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    // Only now: the next kernel's CTAs wait for this kernel with their tensor memory in hand.
+    gptq::let_next_kernel_start();
   }
   gptq::wait_for_previous_kernel();
   if (threadIdx.x == 0)

@@ -96,7 +96,6 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %clusterid.x;" : "=r"(cluster_id));
 
-  gptq::let_next_kernel_start();
   if constexpr (C::APART) gptq::cluster_arrive();  // the CTA has started
   if (threadIdx.x == 0) {
     gptq::flag_write(abort_flag, 0);
@@ -121,6 +120,8 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                  "r"(C::TMEM_COLS)
                  : "memory");
     gptq::tmem_relinquish();
+    // Only now: the next kernel's CTAs wait for this kernel with their tensor memory in hand.
+    gptq::let_next_kernel_start();
   }
   gptq::wait_for_previous_kernel();
   if (threadIdx.x == 0) gptq::flag_write(skip_flag, gptq::status_bad(args.status) ? 1 : 0);

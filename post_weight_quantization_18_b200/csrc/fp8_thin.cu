@@ -132,7 +132,6 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
   const uint32_t abort_flag = tmem_slot + 4, skip_flag = tmem_slot + 8;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  gptq::let_next_kernel_start();
   if constexpr (GROUPED) {
     if (threadIdx.x < BM) gptq::flag_write(amax + threadIdx.x * 4, 0);
     gptq::cluster_arrive();  // the CTA has started, its maxima are zero
@@ -161,6 +160,8 @@ fp8_thin_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ThinA
                  "r"(TMEM_COLS)
                  : "memory");
     gptq::tmem_relinquish();
+    // Only now: the next kernel's CTAs wait for this kernel with their tensor memory in hand.
+    gptq::let_next_kernel_start();
   }
   gptq::wait_for_previous_kernel();
   if (threadIdx.x == 0) gptq::flag_write(skip_flag, gptq::status_bad(args.status) ? 1 : 0);
