@@ -16,7 +16,8 @@ constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: 1 / s stays finite
 
 // The kernels here are launched so that one may start while the kernel before it in the stream still
 // runs (fp8_launch): they set up what is their own, then wait for that kernel and its writes. Every
-// thread calls this before it reads or writes memory that a caller owns.
+// thread calls this before it reads or writes memory that a caller owns. That memory may change while the
+// kernel is resident, so pointers to it are not __restrict__, and no load takes the read-only path.
 GPTQ_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the next kernel in the stream start (it waits as above), once every CTA has a thread that came here. A
 // kernel that needs tensor memory has it by then: otherwise the next one could take an SM's and wait.

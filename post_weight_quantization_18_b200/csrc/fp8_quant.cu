@@ -57,8 +57,8 @@ __device__ __forceinline__ uint2 quantize8(const Vec8<T>& v, float inv) {
 // instead of 7.4 us), so rows of eight groups and more are not split.
 template <typename T, bool IN_ROW>
 __global__ void __launch_bounds__(kRowsThreads)
-quantize_rows_kernel(const T* __restrict__ X, long long ldx, long long items, int groups, int k,
-                     uint8_t* __restrict__ Q, long long ldq, float* __restrict__ S, long long lds,
+quantize_rows_kernel(const T* X, long long ldx, long long items, int groups, int k,
+                     uint8_t* Q, long long ldq, float* S, long long lds,
                      bool vec_x, bool vec_q) {
   gptq::let_next_kernel_start();
   gptq::wait_for_previous_kernel();
@@ -119,8 +119,8 @@ quantize_rows_kernel(const T* __restrict__ X, long long ldx, long long items, in
 // 8 j .. 8 j + 7 of rows i, i + 16, ...
 template <typename T>
 __global__ void __launch_bounds__(256)
-quantize_blocks_kernel(const T* __restrict__ X, long long ldx, int m, int k, int groups,
-                       uint8_t* __restrict__ Q, long long ldq, float* __restrict__ S,
+quantize_blocks_kernel(const T* X, long long ldx, int m, int k, int groups,
+                       uint8_t* Q, long long ldq, float* S,
                        long long lds, bool vec_x, bool vec_q) {
   __shared__ uint32_t part[8];
   gptq::let_next_kernel_start();

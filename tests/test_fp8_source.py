@@ -35,3 +35,11 @@ def test_tensor_memory_comes_before_the_next_kernels_start():
         at = text.find("let_next_kernel_start()")
         assert at < 0 or at > text.index("tcgen05.alloc"), name
     assert found == 3
+
+
+def test_no_read_only_loads():
+    """Inputs may still be written by the kernel before while this one is resident, so nothing may promise
+    the compiler that they do not change: no __restrict__, __ldg or ld.global.nc."""
+    for path in SOURCES:
+        found = re.findall(r"__restrict__|__ldg|\.nc\b", code_of(path))
+        assert not found, (os.path.basename(path), found)
