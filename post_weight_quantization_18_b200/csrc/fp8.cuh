@@ -278,8 +278,12 @@ int fp8_launch(void (*kernel)(P...), long long grid, int threads, int smem, int 
   // 48 KB are open to every kernel, its static shared memory included. 64 KB at least are asked for, so that
   // a kernel whose need grows with its rows (the norm: up to that) is asked for once.
   const int most = smem < 64 * 1024 ? 64 * 1024 : smem;
-  if (smem > 47 * 1024 && ensure_smem_attr(reinterpret_cast<const void*>(kernel), most) != 0)
+  auto failed = [] {
+    (void)cudaGetLastError();  // the library's next call would take this one's error for its own
     return GPTQ_ERR_CUDA;
+  };
+  if (smem > 47 * 1024 && ensure_smem_attr(reinterpret_cast<const void*>(kernel), most) != 0)
+    return failed();
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
@@ -293,8 +297,7 @@ int fp8_launch(void (*kernel)(P...), long long grid, int threads, int smem, int 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? 0
-                                                                                  : GPTQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? 0 : failed();
 }
 
 // Clusters of `size` CTAs (2 to 8) of so many threads and bytes of shared memory that the current device

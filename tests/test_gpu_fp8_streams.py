@@ -207,3 +207,38 @@ def test_output_past_32_bits():
     dh = 1.1 * dg * (np.abs(u) + du) + np.abs(o.silu(ref)) * du + np.abs(h) * 8 * 2.0 ** -24
     check_format(codes_of(out.q[-130:]), out.scales[-130:].cpu().numpy(), h, dh)
     assert not (out.q[:-130].view(torch.uint8) & 0x7F).any() and (out.scales[:-130] == 1).all()
+
+
+def test_a_failed_launch_does_not_fail_the_next_call():
+    """A call on a stream whose capture has been invalidated is refused by the runtime; the error is that
+    call's alone, and the library's next one, whose launch is fine, says so."""
+    code = """
+import ctypes, torch, post_weight_quantization_18_b200 as G
+X = torch.randn(40, 512, device="cuda").bfloat16()
+x = G.fp8.empty(40, 512)
+s = torch.cuda.Stream()
+torch.cuda.synchronize()
+rt = ctypes.CDLL("libcudart.so.12")
+raw, graph = ctypes.c_void_p(s.cuda_stream), ctypes.c_void_p()
+assert rt.cudaStreamBeginCapture(raw, 1) == 0
+assert rt.cudaStreamSynchronize(raw) != 0
+with torch.cuda.stream(s):
+    try:
+        G.fp8_quantize(X, x.q, x.scales)
+        print("not refused")
+    except G.GPTQError as e:
+        assert e.code == 4, e.code
+assert rt.cudaStreamEndCapture(raw, ctypes.byref(graph)) != 0
+rt.cudaGetLastError()
+W = torch.randn(8, 256, device="cuda")
+try:
+    G.rtn(W)
+except G.GPTQError as e:
+    print("failed by the call before:", e)
+torch.cuda.synchronize()
+G.fp8_quantize(X, x.q, x.scales)
+torch.cuda.synchronize()
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
