@@ -4,7 +4,7 @@
     x = fp8.quantize_activations(X)                  # [m, k] -> FP8Matrix
     Y = fp8.linear(x, w)                             # [m, n] bf16
     mlp = fp8.GatedMLP.from_weights(gamma, Wg, Wu, Wd)
-    y, h = mlp(x, residual)                          # norm -> gated pair -> down projection
+    y, h = mlp(X, residual)                          # norm -> gated pair -> down projection
 
 As in `layer`, all arithmetic runs in the library's kernels; this module only sizes and allocates
 buffers and orders the calls on the current stream.

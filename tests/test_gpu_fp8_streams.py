@@ -242,3 +242,16 @@ print("ok")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_the_modules_example_runs():
+    """The lines at the top of fp8.py, as they stand there."""
+    import post_weight_quantization_18_b200 as G
+    lines = [l[4:] for l in G.fp8.__doc__.splitlines() if l.startswith("    ")]
+    assert len(lines) >= 4
+    rnd = lambda *s: torch.randn(s, generator=torch.Generator().manual_seed(len(s))).bfloat16().cuda()
+    env = dict(fp8=G.fp8, X=rnd(5, 256), residual=rnd(5, 256), W=rnd(300, 256), gamma=rnd(256),
+               Wg=rnd(384, 256), Wu=rnd(384, 256), Wd=rnd(256, 384))
+    exec("\n".join(lines), env)
+    torch.cuda.synchronize()
+    assert env["Y"].shape == (5, 300) and env["y"].shape == env["h"].shape == (5, 256)
