@@ -342,3 +342,62 @@ def test_norm_takes_gamma_after_the_mean(k, dtype, gdtype):
     G.fp8_add_rmsnorm(X.cuda(), None, gamma.cuda(), 1e-37, None, Q, S)
     assert torch.isfinite(S).all()
     _check_norm_small(X, gamma, np.float32(1e-37), Q, S)
+
+
+# Rows enough that every warp or CTA of the persistent forms takes three and more, the last round ragged: a
+# warp a row with one and two vectors, a CTA a row with one, two and four.
+NORM_ROUNDS = [(15001, 200), (15001, 500), (4001, 2048), (1501, 5120), (1201, 12288)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,k", NORM_ROUNDS)
+def test_norm_over_many_rounds_of_rows(m, k, dtype):
+    """Every row of a long call is what a call of few rows, each in its first round, makes of it; and some
+    rows of the first, a middle and the last round against the oracle."""
+    import post_weight_quantization_18_b200 as G
+    X, R, gamma = _norm_case(m, k, dtype, "fp32", 5)
+    x, r, g = X.cuda(), R.cuda(), gamma.cuda()
+    H, raw_h = padded(m, k, DTYPES[dtype], ld=k + 8)
+    Q, raw_q = padded(m, k, torch.uint8, ld=-(-k // 16) * 16)
+    S, raw_s = padded(m, -(-k // 128), torch.float32, ld=-(-k // 128) + 1)
+    G.fp8_add_rmsnorm(x, r, g, 1e-5, H, Q, S)
+    few = 144
+    for i in range(0, m, few):
+        n = min(few, m - i)
+        h, q, s = torch.empty_like(x[i:i + n]), torch.empty_like(Q[i:i + n]), torch.empty_like(S[i:i + n])
+        G.fp8_add_rmsnorm(x[i:i + n], r[i:i + n], g, 1e-5, h, q, s)
+        assert torch.equal(h, H[i:i + n]) and torch.equal(q, Q[i:i + n]) and torch.equal(s, S[i:i + n]), i
+    for i in (0, m // 2, m - 8):
+        _check_norm(X[i:i + 8], R[i:i + 8], gamma, np.float32(1e-5), H[i:i + 8], Q[i:i + 8], S[i:i + 8],
+                    dtype)
+    assert untouched(raw_h, H) and untouched(raw_q, Q) and untouched(raw_s, S)
+    for which in range(2):                                # in place: H is X, H is R
+        a, b = x.clone(), r.clone()
+        out, q, s = (a, b)[which], torch.empty_like(Q), torch.empty_like(S)
+        G.fp8_add_rmsnorm(a, b, g, 1e-5, out, q, s)
+        assert torch.equal(out, H) and torch.equal(q, Q) and torch.equal(s, S)
+    q, s = torch.empty_like(Q), torch.empty_like(S)       # no residual: R = -0 adds nothing
+    G.fp8_add_rmsnorm(x, None, g, 1e-5, None, q, s)
+    G.fp8_add_rmsnorm(x, torch.full_like(x, -0.0), g, 1e-5, None, Q, S)
+    assert torch.equal(q, Q) and torch.equal(s, S)
+
+
+@pytest.mark.parametrize("m,k,ld", [(15001, 200, 201), (4001, 2048, 2049), (1501, 5119, 5119)])
+def test_norm_over_many_rounds_of_unaligned_rows(m, k, ld):
+    """Rows that 16-byte copies cannot address are loaded when they are due: the same as aligned ones."""
+    import post_weight_quantization_18_b200 as G
+    X, R, gamma = _norm_case(m, k, "bf16", "bf16", 6)
+    x, _ = padded(m, k, torch.bfloat16, ld=ld)
+    x.copy_(X)
+    y, _ = padded(m, k, torch.bfloat16, ld=-(-k // 8) * 8)
+    y.copy_(X)
+    r, _ = padded(m, k, torch.bfloat16, ld=-(-k // 8) * 8)
+    r.copy_(R)
+    outs = []
+    for a in (x, y):
+        q = torch.empty((m, k), dtype=torch.uint8, device="cuda")
+        s = torch.empty((m, -(-k // 128)), device="cuda")
+        G.fp8_add_rmsnorm(a, r, gamma.cuda(), 1e-5, None, q, s)
+        outs.append((q, s))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    _check_norm(X[-8:], R[-8:], gamma, np.float32(1e-5), None, outs[0][0][-8:], outs[0][1][-8:], "bf16")
