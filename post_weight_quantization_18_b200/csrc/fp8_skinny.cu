@@ -19,6 +19,7 @@
 // the kernel's start, the latency of its first load and the cluster's exchange.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-7 epilogue (gated pair: 8-11 the
 // second weight's). Every wait is bounded as in fp8_gemm.cu.
+#include "fp8_exchange.cuh"
 #include "fp8_mma.cuh"
 
 namespace {
@@ -38,10 +39,10 @@ struct Cfg {
   static constexpr int CTAS_PER_SM = NW * MT > 64 ? 1 : 2;
   static constexpr int NBUF = 4;  // accumulators
   static constexpr int STAGE_BYTES = NW * W_TILE + MT * BK;
-  // Where the cluster's sums arrive: the CTA's share of the rows times the CTAs, 36 of 32 at seven. The
-  // plain product has room for it beside the ring, the gated pair uses the ring again.
+  // Where the cluster's sums arrive: the CTA's share of the rows times the CTAs. The plain product has room
+  // for it beside the ring, the gated pair uses the ring again.
   static constexpr bool APART = NW == 1;
-  static constexpr int SUMS = (MT + 5) * NW * BM * 4, RECV = APART ? SUMS : 0;
+  static constexpr int SUMS = gptq::exchange_rows(MT) * NW * BM * 4, RECV = APART ? SUMS : 0;
   static constexpr int STAGES = 
       (228 * 1024 / CTAS_PER_SM - 1024 - 1024 - 512 - RECV - Scales::BYTES) / STAGE_BYTES;
   static constexpr int RING = STAGES * STAGE_BYTES;
@@ -299,15 +300,15 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
       const int r = (int)rank + i * args.ksplit;
       if (r >= args.M) break;
       const uint32_t from = recv + (uint32_t)(i * args.ksplit * NW * BM + lane * 4) * 4;
-      float4 p[8][NW];
+      float4 p[gptq::kMaxSplit][NW];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
+      for (int s = 0; s < gptq::kMaxSplit; ++s)
         if (s < args.ksplit) {
 #pragma unroll
           for (int j = 0; j < NW; ++j) p[s][j] = gptq::lds_f32x4(from + (s * NW + j) * (BM * 4));
         }
 #pragma unroll
-      for (int s = 1; s < 8; ++s)
+      for (int s = 1; s < gptq::kMaxSplit; ++s)
         if (s < args.ksplit) {
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
@@ -381,7 +382,7 @@ int fp8_skinny(const Fp8Gemm& g, cudaStream_t stream) {
   // of 8 of the 33 there are: 6.8 us, of 7: 6.3, of 6: 6.0; 1 x 8192 x 8192 in 64 of 4 of 71: 14.2, of 3:
   // 13.4; but 16 x 11008 x 4096 in 86 of 3: 10.3, of 2: 11.6; gated 1 x 4096 x 4096 of 7: 9.5, of 6: 9.8).
   auto run = [&](auto launch, int threads, int smem) {
-    a.ksplit = a.nkb >= 32 ? 8 : a.nkb >= 8 ? a.nkb / 4 : 1;
+    a.ksplit = a.nkb >= 4 * gptq::kMaxSplit ? gptq::kMaxSplit : a.nkb >= 8 ? a.nkb / 4 : 1;
     auto fits = [&](int s) {
       return blocks + (s > 3 ? blocks / (gated ? 8 : 4) : 0) <= resident_clusters(threads, smem, s);
     };
