@@ -9,16 +9,32 @@ extension importing this module raises.
 from __future__ import annotations
 
 import os
+import re
+import sys
+
+import torch
 
 from . import _lib
 
-try:
-    from . import _fp8_binding
-except ImportError as e:
+
+def _load():
+    """The extension module, compiled for the torch and Python at hand: it reads objects by their layout."""
+    try:
+        from . import _fp8_binding
+    except ImportError as e:
+        why = e
+    else:
+        version = re.match(r"[0-9.]*[0-9]", torch.__version__).group()
+        here = f"torch {version}, Python {sys.version_info.major}.{sys.version_info.minor}"
+        if here == _fp8_binding.built_for:
+            return _fp8_binding
+        why = f"it was built for {_fp8_binding.built_for}, this is {here}"
     raise ImportError(
-        f"{os.path.join(os.path.dirname(_lib.LIB_PATH), '_fp8_binding.so')} cannot be loaded ({e}): "
-        "build it with `python post_weight_quantization_18_b200/build.py` (there is no CPU fallback)"
-    ) from e
+        f"{os.path.join(os.path.dirname(_lib.LIB_PATH), '_fp8_binding.so')} cannot be loaded ({why}): "
+        "build it with `python post_weight_quantization_18_b200/build.py` (there is no CPU fallback)")
+
+
+_fp8_binding = _load()
 
 GPTQ_F16 = 2
 

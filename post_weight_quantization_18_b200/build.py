@@ -14,7 +14,7 @@ extension module that calls the library's 8-bit floating point operators.
 from __future__ import annotations
 
 import glob
-import importlib.util
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -29,6 +29,7 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgptq_b200.so")
 BINDING = os.path.join(HERE, "_fp8_binding.so")
 BINDING_SRC = os.path.join(CSRC, "fp8_binding.cpp")
+BINDING_FOR = os.path.join(OBJDIR, "_fp8_binding.for")   # the torch and Python it was compiled for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -58,9 +59,17 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def binding_abi() -> str:
+    """What the binding's machine code depends on beside its source: torch's C++ layout and Python's."""
+    return f"torch {importlib.metadata.version('torch')} {sysconfig.get_config_var('SOABI')}\n"
+
+
 def binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING):
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_FOR):
         return False
+    with open(BINDING_FOR) as f:
+        if f.read() != binding_abi():
+            return False
     t = os.path.getmtime(BINDING)
     return all(os.path.getmtime(p) <= t
                for p in [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
@@ -68,11 +77,14 @@ def binding_up_to_date() -> bool:
 
 def build_binding() -> None:
     """_fp8_binding.so from csrc/fp8_binding.cpp (the library has to be there: it is linked)."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    os.makedirs(OBJDIR, exist_ok=True)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(torch_dir, "include"),
            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
@@ -82,6 +94,8 @@ def build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(binding_abi())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cstdarg>
 #include <cstdio>
@@ -303,4 +304,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fp8_binding",
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fp8_binding() { return PyModule_Create(&g_module); }
+// With the torch and the Python whose headers it was compiled against: it reads objects by their layout.
+PyMODINIT_FUNC PyInit__fp8_binding() {
+  PyObject* m = PyModule_Create(&g_module);
+  char built_for[64];
+  snprintf(built_for, sizeof built_for, "torch %s, Python %d.%d", TORCH_VERSION, PY_MAJOR_VERSION,
+           PY_MINOR_VERSION);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", built_for) != 0) Py_CLEAR(m);
+  return m;
+}

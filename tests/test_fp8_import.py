@@ -61,3 +61,29 @@ def test_everything_with_the_binding(tmp_path):
     copy_of_package(tmp_path, os.path.join(PKG, "_fp8_binding.so"))
     r = run(tmp_path, f"import {NAME} as G; print(callable(G.fp8_gemm), G.fp8.__name__)")
     assert r.returncode == 0 and r.stdout.strip() == f"True {NAME}.fp8", r.stdout + r.stderr
+
+
+def test_binding_of_another_torch_is_refused(tmp_path):
+    """It reads tensors by the layout it was compiled against. Without a torch of another version at hand, the
+    version that this one reports is changed."""
+    copy_of_package(tmp_path, os.path.join(PKG, "_fp8_binding.so"))
+    r = run(tmp_path, "import torch; torch.__version__ = '1.13.1+cu117'\n" + USE)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(built, monkeypatch):
+    import importlib.metadata
+    import sysconfig
+
+    import __graft_entry__
+    build = __graft_entry__._build_module()
+    assert build.binding_up_to_date()
+    with monkeypatch.context() as mp:
+        version = importlib.metadata.version
+        mp.setattr(importlib.metadata, "version", lambda n: "1.13.1" if n == "torch" else version(n))
+        assert not build.binding_up_to_date()
+    with monkeypatch.context() as mp:
+        get = sysconfig.get_config_var
+        mp.setattr(sysconfig, "get_config_var", lambda n: "cpython-38" if n == "SOABI" else get(n))
+        assert not build.binding_up_to_date()
+    assert build.binding_up_to_date()
