@@ -13,6 +13,7 @@ extension module that calls the library's 8-bit floating point operators.
 """
 from __future__ import annotations
 
+import fcntl
 import glob
 import importlib.metadata
 import os
@@ -79,7 +80,6 @@ def build_binding() -> None:
     """_fp8_binding.so from csrc/fp8_binding.cpp (the library has to be there: it is linked)."""
     import torch
     torch_dir = os.path.dirname(torch.__file__)
-    os.makedirs(OBJDIR, exist_ok=True)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
@@ -99,9 +99,14 @@ def build_binding() -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_library(force, verbose)
-    if force or not binding_up_to_date():
-        build_binding()
+    if not force and up_to_date() and binding_up_to_date():
+        return LIB
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(os.path.join(OBJDIR, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)   # until closed: processes that build at once take turns
+        build_library(force, verbose)
+        if force or not binding_up_to_date():
+            build_binding()
     return LIB
 
 
