@@ -255,3 +255,86 @@ def test_the_modules_example_runs():
     exec("\n".join(lines), env)
     torch.cuda.synchronize()
     assert env["Y"].shape == (5, 300) and env["y"].shape == env["h"].shape == (5, 256)
+
+
+def test_capture_that_forks_and_joins():
+    """A captured call whose operands come from two streams, from a copy, and from a fill: it waits for all of
+    them at every replay, whatever was left in the buffers."""
+    import post_weight_quantization_18_b200 as G
+    m, n, k = 70, 640, 1024
+    g = torch.Generator().manual_seed(20)
+    rnd = lambda *s: torch.randn(s, generator=g).bfloat16().cuda()
+    Xs, Ws, Vs = [rnd(m, k) for _ in range(3)], [rnd(n, k) for _ in range(3)], [rnd(n, k) for _ in range(3)]
+    X, W, V = torch.empty_like(Xs[0]), torch.empty_like(Ws[0]), torch.empty_like(Vs[0])
+    x, w, v = G.fp8.empty(m, k), G.fp8.empty(n, k, 128), G.fp8.empty(n, k, 128)
+    hid, copy = G.fp8.empty(m, n), G.fp8.empty(m, n)
+    y = torch.empty((m, k), device="cuda")
+    down, = _weights(k, n, 21)
+
+    def body(side):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            G.fp8_quantize(W, w.q, w.scales, 128)
+            G.fp8_quantize(V, v.q, v.scales, 128)
+        G.fp8_quantize(X, x.q, x.scales)
+        main.wait_stream(side)                            # two kernels ahead, one in each stream
+        G.fp8_gated_gemm(x.q, x.scales, w.q, w.scales, v.q, v.scales, hid.q, hid.scales)
+        copy.q.view(torch.uint8).copy_(hid.q.view(torch.uint8))
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            copy.scales.copy_(hid.scales)                 # a copy ahead, in the other stream
+        main.wait_stream(side)
+        G.fp8_gemm(copy.q, copy.scales, down.q, down.scales, y)
+        x.scales.zero_()                                  # a fill behind, and ahead of the next call
+        G.fp8_gemm(x.q, x.scales, w.q, w.scales, z)
+    z = torch.empty((m, n), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body(torch.cuda.Stream())
+    for i in range(12):
+        for b in (y, z, hid.scales, copy.scales, w.scales, v.scales):
+            b.fill_(float("nan"))
+        X.copy_(Xs[i % 3]); W.copy_(Ws[(i + 1) % 3]); V.copy_(Vs[(i + 2) % 3])
+        graph.replay()
+        torch.cuda.synchronize()
+        a = G.fp8.quantize_activations(Xs[i % 3])
+        h = G.fp8.gated(a, G.fp8.quantize_weight(Ws[(i + 1) % 3]), G.fp8.quantize_weight(Vs[(i + 2) % 3]))
+        torch.cuda.synchronize()
+        assert torch.equal(y, G.fp8.linear(h, down, torch.float32)), i
+        assert (z == 0).all(), i
+
+
+def test_calls_from_several_threads():
+    """Four threads with a stream each, every size of call among them, first calls of the process included."""
+    code = """
+import threading, torch, post_weight_quantization_18_b200 as G
+sizes = [(1, 512, 2048), (20, 1024, 1024), (50, 4864, 512), (100, 640, 4096), (300, 2048, 512)]
+g = torch.Generator().manual_seed(1)
+data = [[torch.randn(s, generator=g).bfloat16().cuda() for s in ((m, k), (n, k), (n, k))] for m, n, k in sizes]
+out = {}
+torch.cuda.synchronize()
+def work(t):
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for i in range(40):
+            X, W, V = data[(i + t) % len(data)]
+            w, v = G.fp8.quantize_weight(W), G.fp8.quantize_weight(V)
+            x, _ = G.fp8.add_rmsnorm(X, None, torch.ones(X.shape[1], device="cuda"))
+            h = G.fp8.gated(x, w, v)
+            y = G.fp8.linear(x, w)
+            out.setdefault((i + t) % len(data), []).append((h.q.view(torch.uint8), h.scales, y))
+        torch.cuda.current_stream().synchronize()
+ts = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+[t.start() for t in ts]; [t.join() for t in ts]
+torch.cuda.synchronize()
+n = 0
+for i, (X, W, V) in enumerate(data):
+    want = out[i][0]
+    assert torch.isfinite(want[2]).all()
+    for got in out[i]:
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), i
+        n += 1
+print(n)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "160", r.stdout + r.stderr
