@@ -59,7 +59,7 @@ int fp8_quantize(const void* X, int x_dtype, int64_t ldx, int64_t m, int64_t k, 
  * fp8_add_rmsnorm — the residual's addition, the root-mean-square norm and the quantization:
  *   h = x + r            in fp32 (h = x when R is NULL)
  *   H = h                rounded to dtype (not written when H is NULL)
- *   y = h / sqrt(mean_j(h_j^2) + eps) * gamma      in fp32, from the unrounded h
+ *   y = h / sqrt(mean_j(h_j^2) + eps) * gamma      in fp32, in this order, from the unrounded h
  *   Q, scales = y in the format, one scale per row and 128 columns
  *
  *   X, R, H     [m, ld] of `dtype` (GPTQ_BF16, GPTQ_F16, GPTQ_F32). H may be X or R itself (the
@@ -80,7 +80,8 @@ int fp8_add_rmsnorm(const void* X, int64_t ldx, const void* R, int64_t ldr, int 
  *   Y[i, j] = sum_g sx[i, g] * sw[j / 128, g] * sum_{c in block g} X[i, c] * W[j, c]
  * with exact products, the sum over each block of 128 columns in the tensor core's fp32
  * accumulator and the scaled sums added in fp32; rounded once to y_dtype (a value beyond fp16's
- * range becomes an infinity).
+ * range becomes an infinity). sx * sw is formed first, in fp32: beyond 3.4e38 it is an infinity, and
+ * below 2^-126 it has fewer bits.
  *
  *   X           e4m3 [m, ldx], sx fp32 [m, ldsx]                (blocks of 1 x 128)
  *   W           e4m3 [n, ldw], sw fp32 [ceil(n / 128), ldsw]    (blocks of 128 x 128)

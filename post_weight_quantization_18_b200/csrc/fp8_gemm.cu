@@ -19,10 +19,12 @@
 // (bounded) for the loads and MMAs it already issued before it frees TMEM and exits.
 //
 // Measured (B200): 8192 x 8192 x 28672 in 1.86 to 1.93 ms, 2.0 PFLOP/s, at 1335 MHz under the 1 kW
-// power limit, which bounds it: without reading and scaling the accumulators the same pipeline
-// takes 1.47 ms, the reads add 0.12, the multiply-adds 0.26. 2048 x 4096 x 4096: 34 us, tensor pipe
-// 52 % busy (a block of K waits for the epilogue, 256 of its 512 cycles are multiply-adds). A
-// 128 x 256 tile per CTA with the same loops: 2.3 ms.
+// power limit. Two things bound it. The clock is the power's; and of the cycles at that clock the tensor
+// pipe is busy 50 to 60 % (2048 x 4096 x 4096, 34 us: 52 %; gated 2000 x 6912 x 5120: 57 %), because a block
+// of K takes the pair about 800 cycles, of which the MMAs are 512: they wait until the epilogue has read
+// an accumulator, all eight loads of it. Without reading and scaling the accumulators the same pipeline
+// takes 1.47 ms, the reads add 0.12, the multiply-adds 0.26. A 128 x 256 tile per CTA with the same
+// loops: 2.3 ms.
 #include "fp8_mma.cuh"
 
 namespace {

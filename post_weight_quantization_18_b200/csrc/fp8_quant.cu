@@ -4,9 +4,10 @@
 //
 // All three read each input once and write each output once; a block's largest magnitude is
 // found in registers before anything is written. They are bound by HBM, and next by the number of
-// instructions (issue slots 60 to 75 % busy). Measured (B200, measured copy rate 6.44 TB/s):
-// weights 8192 x 28672 bf16 in 102 us (6.9 TB/s), rows 4096 x 11008 fp16 in 22.8 us (5.9), norm
-// 8192 x 5120 bf16 in 52 us (5.6; its registers allow three CTAs of 320 threads an SM).
+// instructions (issue slots 60 to 75 % busy). Measured (B200, measured copy rate 6.44 TB/s), in a graph of
+// calls over inputs larger than L2 and, behind the stroke, called one after the other from Python:
+// weights 8192 x 28672 bf16 in 102 / 107 us (6.9 TB/s), rows 4096 x 11008 fp16 in 22.9 / 24.8 us (5.9),
+// norm 8192 x 5120 bf16 in 51.3 / 54.4 us (5.7; its registers allow three CTAs of 320 threads an SM).
 #include "fp8.cuh"
 
 namespace {
@@ -239,7 +240,7 @@ template <typename T, typename TG, int V, bool TEAM_WARP>
 __global__ void __launch_bounds__(512, 2) add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   constexpr bool AHEAD = sizeof(T) == 2;
   // gamma before the row's sum, but not where registers are short: with four vectors they are better
-  // spent on a second CTA (8192 x 8704 of bf16: 137 us, so 97)
+  // spent on a second CTA (8192 x 8704 of bf16: 137 us, so 99)
   constexpr bool EARLY = (AHEAD && V < 4) || V == 1;
   extern __shared__ __align__(16) uint8_t next_row[];  // [x, r][V][threads] of 16 bytes
   __shared__ float part[2][32];

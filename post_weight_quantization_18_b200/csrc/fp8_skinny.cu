@@ -13,10 +13,13 @@
 // warp adds them up, always in the same order; for the gated pair it also has the whole 128
 // columns of the row's scale.
 // Two CTAs share an SM, so that one's start and end pass behind the other's stream.
-// Measured (B200): 1 x 8192 x 28672 in 37.3 us (6.3 TB/s, 0.98 of the measured copy rate), 8 x 11008 x
-// 4096 gated in 18.0 us (5.0 TB/s), 64 x 11008 x 4096 gated in 21.3 us, 16 x 11008 x 4096 in 10.3 us (what
-// a loop that only streams this weight takes), 1 x 4096 x 4096 in 6.0 us, of which more than 3 are
-// the kernel's start, the latency of its first load and the cluster's exchange.
+// Measured (B200, weights larger than L2 in a graph of calls): 1 x 8192 x 28672 in 38.7 us (6.1 TB/s, 0.94
+// of the measured copy rate), 8 x 11008 x 4096 gated in 18.0 us (5.0 TB/s), 16 x 11008 x 4096 in 10.4 us
+// (what a loop that only streams this weight takes), 1 x 4096 x 4096 in 6.0 us, of which more than 3 are
+// the kernel's start, the latency of its first load and the cluster's exchange (weights in L2: 5.4).
+// Further from their floors: 32 x 11008 x 4096 in 11.1 us (floor 7.1; four stages, with 16 rows five), gated 64 x
+// 11008 x 4096 in 21.5 us and 32 x 11008 x 4096 in 21.0 (floor 14.1). The last, Cfg<2, 32>, is the poorest
+// variant: two stages, a third 1280 bytes short of the shared memory, and 16 bytes of registers spilled.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-7 epilogue (gated pair: 8-11 the
 // second weight's). Every wait is bounded as in fp8_gemm.cu.
 #include "fp8_exchange.cuh"

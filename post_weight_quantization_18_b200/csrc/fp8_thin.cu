@@ -16,7 +16,7 @@
 //                      and added up there, always in the same order. Gated:
 //                      h is made where its sums are, a row's maximum goes round the cluster.
 // Measured (B200): 64 x 8192 x 28672 in 45 us (5.3 TB/s), 64 x 11008 x 4096 in 12.0 us (a loop that
-// only streams this weight: 10.3), 512 x 4096 x 4096 in 12.8 us, gated 100 x 11008 x 4096 in 24.1 us.
+// only streams this weight: 10.3), 512 x 4096 x 4096 in 13.0 us, gated 100 x 11008 x 4096 in 24.5 us.
 // Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 scales, 4-11 epilogue (two per quarter of the TMEM
 // lanes, half the tile's columns each). Every wait is bounded as in fp8_gemm.cu.
 #include <cudaTypedefs.h>
@@ -721,7 +721,7 @@ long long fp8_thin_cost(const Fp8Gemm& g) {
   const int sms = num_sms();
   if (g.w[1] == nullptr) return tile_cost(g, plain_tile(g, sms), sms);
   // Gated pair: 32 or 64 rows of each weight where clusters hold all groups (100 x 4096 x 4096: 13.1 us, a
-  // block 0.33), else 128 (100 x 11008 x 4096: 24.1 us, a block 0.6).
+  // block 0.33), else 128 (100 x 11008 x 4096: 24.5 us, a block 0.6).
   const long long groups = (long long)((g.m + BM - 1) / BM) * ((g.n + 127) / 128);
   if (groups <= resident(4)) return 195;
   if (groups <= resident(2)) return 300;
