@@ -26,9 +26,10 @@ def _load():
     else:
         version = re.match(r"[0-9.]*[0-9]", torch.__version__).group()
         here = f"torch {version}, Python {sys.version_info.major}.{sys.version_info.minor}"
-        if here == _fp8_binding.built_for:
+        built_for = getattr(_fp8_binding, "built_for", "an earlier version")
+        if here == built_for:
             return _fp8_binding
-        why = f"it was built for {_fp8_binding.built_for}, this is {here}"
+        why = f"it was built for {built_for}, this is {here}"
     raise ImportError(
         f"{os.path.join(os.path.dirname(_lib.LIB_PATH), '_fp8_binding.so')} cannot be loaded ({why}): "
         "build it with `python post_weight_quantization_18_b200/build.py` (there is no CPU fallback)")

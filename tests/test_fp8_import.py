@@ -87,3 +87,11 @@ def test_binding_is_rebuilt_for_another_torch_or_python(built, monkeypatch):
         mp.setattr(sysconfig, "get_config_var", lambda n: "cpython-38" if n == "SOABI" else get(n))
         assert not build.binding_up_to_date()
     assert build.binding_up_to_date()
+
+
+def test_binding_that_does_not_say_what_it_was_built_for(tmp_path):
+    """One from before it did, left by an update of the sources without a build."""
+    dst = copy_of_package(tmp_path)
+    (dst / "_fp8_binding.py").write_text("def set_error(e): pass\n")
+    r = run(tmp_path, USE)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
